@@ -26,7 +26,8 @@
  *   - Launch log: with the environment variable PQL_LOG set to anything but
  *     "" or "0" (read once, at the first call), pql_quantize,
  *     pql_quantize_static, pql_dequantize, pql_qgemm(_ex), pql_qlinear(_ex),
- *     pql_qlinear_noalloc and pql_repack each write one line to stderr: the
+ *     pql_qlinear_noalloc, pql_repack and the expert calls (pql_moe_*,
+ *     pql_swiglu_quantize) each write one line to stderr: the
  *     call, scheme, role and shape, then the kernel enqueued (the name
  *     pql_kernel_name gives) and the stream, "nothing to do" for an empty
  *     operand, or "rejected (status S)" with the pql_last_error() text.
@@ -316,6 +317,98 @@ size_t pql_noalloc_scratch_bytes(void);
 /* Name of the kernel that `op` would launch for these sizes (for "no silent
  * fallback" checks); "" if the combination is invalid.  Static string. */
 const char* pql_kernel_name(int op, int scheme, int role, int64_t M, int64_t N, int64_t K);
+
+/* ------------------------------------------------------------------ experts
+ * The layer of experts around the quantized linear: a router picks k of E
+ * experts for each of T tokens, the P = T * k assignments are grouped by
+ * expert, every expert's rows are multiplied with its own quantized weight,
+ * and the results are summed back to tokens.  One pass, in order:
+ *   pql_moe_route -> pql_moe_plan -> pql_quantize (T rows) -> pql_moe_qgemm
+ *   (gather) -> pql_swiglu_quantize -> pql_moe_qgemm -> pql_moe_combine
+ * Nothing is read back to the host in between: the group sizes stay on the
+ * device, so the whole pass can be captured into a HIP graph.
+ * Limits: 1 <= E <= 1024, 1 <= k <= 32, T * k <= 2^24 - 1. */
+
+/* Element types of router logits. */
+typedef enum pql_dtype { PQL_F32 = 0, PQL_BF16 = 1, PQL_F16 = 2 } pql_dtype;
+
+/* Scores of the experts from the logits x[t, :]: softmax over all E, or a
+ * sigmoid of each. */
+typedef enum pql_moe_score { PQL_MOE_SOFTMAX = 0, PQL_MOE_SIGMOID = 1 } pql_moe_score;
+
+/* Score of a group of experts: its highest choice, or the sum of its two
+ * highest (of the one, where only one is available). */
+typedef enum pql_moe_group { PQL_MOE_GROUP_MAX = 0, PQL_MOE_GROUP_TOP2 = 1 } pql_moe_group;
+
+/* The k experts of each token and their weights.
+ *   s = softmax(x) or sigmoid(x);  the choice is s + bias[e] with a bias (fp32
+ *   [E], for balance; it decides who is chosen, not the weight), formed in
+ *   64 bits, and the order of the logits themselves without one.
+ *   With groups > 1 (E / groups consecutive experts each) only the experts of
+ *   the top_groups groups with the highest group scores take part.
+ *   ids[t, 0..k-1]: the experts of highest choice, best first; equal choices
+ *   go to the lowest index (experts and groups alike).
+ *   weights[t, j] = s of ids[t, j], divided by the sum over the k if
+ *   `renormalize` (0 where that sum is 0), times `scale`.
+ * A logit of -inf (or a bias of -inf or NaN) makes an expert unavailable;
+ * slots for which no expert is left get id -1 and weight 0.  A row that holds
+ * a NaN or +inf gets id -1 and weight NaN in every slot, and
+ * pql_moe_combine then gives NaN for that token.
+ * logits: [T, E], row stride ldl >= E, aligned to its element type.  ids
+ * (int32) and weights (fp32): [T, k], contiguous.  T = 0 is a no-op. */
+pql_status pql_moe_route(int score, int dtype, const void* logits, int64_t T, int64_t E, int64_t ldl,
+                         const float* bias, int64_t k, int64_t groups, int64_t top_groups, int group_score,
+                         int renormalize, float scale, int32_t* ids, float* weights, void* stream);
+
+/* Workspace bytes of pql_moe_plan (host output; may be 0). */
+pql_status pql_moe_plan_workspace(int64_t T, int64_t k, int64_t E, size_t* bytes);
+
+/* Group the assignments i = t * k + j (ids[i], [T, k] contiguous) by expert,
+ * in order of i within an expert.  An id outside 0 .. E - 1 (an expert held
+ * elsewhere, or none) takes no part.
+ *   offsets int32 [E + 1]: expert e has positions offsets[e] .. offsets[e+1]-1
+ *   order   int32 [P]: order[p] = i for the position p; -1 from offsets[E] on
+ *   slots   int32 [P]: slots[i] = p, or -1 where the id takes no part
+ * T = 0 writes zero offsets.  The result is the same on every run. */
+pql_status pql_moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offsets, int32_t* order,
+                        int32_t* slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The experts' products, FP8_ROW and FP8_BLOCK128:
+ *   C[p, n] = bf16( sum_k a_hat[row(p), k] w_hat[e * N + n, k] )
+ * for every position p < offsets[E], e the expert whose range holds p,
+ * fp32 accumulation as in pql_qgemm.  gather != 0: row(p) = order[p] / k, the
+ * assignment's token (the activation has T rows); gather = 0: row(p) = p (T * k
+ * rows, order may be NULL).  w_codes / w_scales: the E weights [N, K] stacked,
+ * i.e. what pql_quantize writes for the [E * N, K] weight (FP8_BLOCK128 needs
+ * N % 128 == 0).  Rows of C from offsets[E] on are left as they were.  offsets
+ * and order are pql_moe_plan's; values outside their ranges are clamped, never
+ * followed.  K % 128 == 0, N <= 2^20. */
+pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,
+                         const void* w_codes, const void* w_scales, const int32_t* offsets, const int32_t* order,
+                         int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, void* c, int64_t ldc, void* stream);
+
+/* Gated activation and quantization in one pass, FP8_ROW and FP8_BLOCK128:
+ *   h[r, c] = silu(x[r, c]) * x[r, cols + c],  silu(g) = g / (1 + exp(-g)),
+ * from a bf16 [rows, 2 * cols] tensor (gate half, then up half; row stride ldx),
+ * kept in fp32, then quantized by the scheme's activation rule into codes and
+ * scales as pql_quantize lays them out.  row_count (device int32, or NULL): rows
+ * from *row_count on are left as they were -- offsets + E of a plan, so that
+ * positions of experts held elsewhere cost nothing.  h must be finite.  rows <= 2^24 - 1;
+ * rows = 0 is a no-op. */
+pql_status pql_swiglu_quantize(int scheme, const void* x, int64_t rows, int64_t cols, int64_t ldx,
+                               const int32_t* row_count, void* codes, void* scales, void* stream);
+
+/* out[t, n] = bf16( add[t, n] + sum_j weights[t, j] * y[slots[t * k + j], n] )
+ * in fp32, j ascending, `add` (bf16 [T, N], a shared expert's output or a
+ * residual; may be `out` itself) last, one rounding.  A slot outside
+ * 0 .. y_rows - 1 contributes weights[t, j] * 0.  Row strides in elements, any
+ * value >= N; rows that all start on 16 bytes with N % 8 == 0 run fastest. */
+pql_status pql_moe_combine(const void* y, int64_t y_rows, int64_t ldy, const int32_t* slots, const float* weights,
+                           int64_t T, int64_t k, int64_t N, const void* add, int64_t ldadd, void* out, int64_t ldo,
+                           void* stream);
+
+/* Name of the kernel pql_moe_qgemm would launch; "" if the combination is invalid. */
+const char* pql_moe_kernel_name(int scheme, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }

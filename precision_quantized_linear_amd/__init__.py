@@ -64,7 +64,16 @@ def lib() -> ctypes.CDLL:
         L.pql_repack.argtypes = [ci, ci, ci, ci, vp, vp, vp, vp, i64, i64, vp]
         L.pql_qlinear_noalloc.argtypes = [ci, vp, i64, i64, i64, vp, vp, vp, vp, i64, f32, vp, vp, i64, vp]
         L.pql_noalloc_scratch_bytes.restype = sz
-        for f in ("pql_quantized_sizes", "pql_workspace_size", "pql_quantize", "pql_dequantize",
+        L.pql_moe_kernel_name.restype = ctypes.c_char_p
+        L.pql_moe_kernel_name.argtypes = [ci, i64, i64, i64, i64, i64]
+        L.pql_moe_route.argtypes = [ci, ci, vp, i64, i64, i64, vp, i64, i64, i64, ci, ci, f32, vp, vp, vp]
+        L.pql_moe_plan_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+        L.pql_moe_plan.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.pql_moe_qgemm.argtypes = [ci, vp, vp, i64, ci, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp]
+        L.pql_swiglu_quantize.argtypes = [ci, vp, i64, i64, i64, vp, vp, vp, vp]
+        L.pql_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp, i64, vp]
+        for f in ("pql_moe_route", "pql_moe_plan_workspace", "pql_moe_plan", "pql_moe_qgemm", "pql_swiglu_quantize",
+                  "pql_moe_combine", "pql_quantized_sizes", "pql_workspace_size", "pql_quantize", "pql_dequantize",
                   "pql_qgemm", "pql_qlinear", "pql_quantize_static", "pql_qgemm_ex", "pql_qlinear_ex",
                   "pql_qlinear_noalloc", "pql_layout_sizes", "pql_repack"):
             getattr(L, f).restype = ci
@@ -516,3 +525,244 @@ def qlinear_noalloc(x: torch.Tensor, w: QTensor, out: torch.Tensor, alpha: float
 
 def noalloc_scratch_bytes() -> int:
     return int(lib().pql_noalloc_scratch_bytes())
+
+
+# ---------------------------------------------------------------- experts
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_GROUP_SCORES = {"max": 0, "top2": 1}
+MOE_SCHEMES = ("fp8_row", "fp8_block128")
+_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+@dataclass
+class MoePlan:
+    """The assignments i = token * top_k + j of a batch, grouped by expert (include/pql.h,
+    pql_moe_plan): int32 ``offsets`` [n_experts + 1], ``order`` [tokens * top_k] (position to
+    assignment) and ``slots`` [tokens * top_k] (assignment to position, -1 for none)."""
+    tokens: int
+    top_k: int
+    n_experts: int
+    offsets: torch.Tensor
+    order: torch.Tensor
+    slots: torch.Tensor
+
+    @property
+    def device(self):
+        return self.offsets.device
+
+
+class _device_of:
+    """Make a tensor's device current for a launch; nothing where it already is."""
+
+    def __init__(self, device):
+        self.index = device.index
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _check_vector(t, name: str, dtype, n: int, device) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the operands on {device}")
+
+
+def _check_plan(plan, device=None) -> None:
+    if not isinstance(plan, MoePlan):
+        raise ValueError("plan must be a MoePlan")
+    device = plan.device if device is None else device
+    _check_vector(plan.offsets, "plan.offsets", torch.int32, plan.n_experts + 1, device)
+    _check_vector(plan.order, "plan.order", torch.int32, plan.tokens * plan.top_k, device)
+    _check_vector(plan.slots, "plan.slots", torch.int32, plan.tokens * plan.top_k, device)
+
+
+def _check_moe_scheme(scheme: str) -> None:
+    if scheme not in MOE_SCHEMES:
+        raise NotImplementedError(f"defined for the schemes {MOE_SCHEMES}, not {scheme!r}")
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+              n_groups: int = 1, top_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
+              scale: float = 1.0):
+    """The ``top_k`` experts of each token, best first, and their weights: int32 and float32
+    [T, top_k] from router logits [T, E] (fp32, bf16 or fp16; any row stride).
+
+    ``score``: "softmax" or "sigmoid".  ``bias`` (float32 [E]) is added to the scores for the
+    choice alone.  With ``n_groups`` > 1 only the ``top_groups`` best groups of E / n_groups
+    consecutive experts take part (``group_score``: a group's "max" choice, or the sum of its
+    "top2").  Ties go to the lowest index.  ``renormalize`` divides the weights by their sum,
+    ``scale`` multiplies them.  Unavailable experts (-inf) and broken rows (NaN, +inf): see
+    include/pql.h, pql_moe_route."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGIT_TYPES:
+        raise ValueError("logits must be a float32, bfloat16 or float16 tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-D with unit stride along the experts")
+    if score not in MOE_SCORES:
+        raise ValueError(f"unknown score {score!r}; supported: {sorted(MOE_SCORES)}")
+    if group_score not in MOE_GROUP_SCORES:
+        raise ValueError(f"unknown group score {group_score!r}; supported: {sorted(MOE_GROUP_SCORES)}")
+    T, E = logits.shape
+    device = logits.device
+    if bias is not None:
+        _check_vector(bias, "bias", torch.float32, E, device)
+    _on_device(device)
+    k = int(top_k)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
+    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
+    ld = logits.stride(0) if T > 1 else E
+    with _device_of(device):
+        _check(lib().pql_moe_route(MOE_SCORES[score], _LOGIT_TYPES[logits.dtype], logits.data_ptr(), T, E, ld,
+                                   _ptr(bias), k, n_groups, top_groups, MOE_GROUP_SCORES[group_score],
+                                   int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
+                                   _stream(device)), "moe_route")
+    return ids, weights
+
+
+def moe_plan(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | None = None) -> MoePlan:
+    """Group the assignments of int32 ids [T, top_k] by expert (stable).  Ids outside
+    0 .. n_experts - 1 take no part: experts held elsewhere, or none."""
+    if not isinstance(ids, torch.Tensor) or ids.dtype != torch.int32 or ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T, top_k] tensor")
+    T, k = ids.shape
+    device = ids.device
+    _on_device(device)
+    wsb = ctypes.c_size_t()
+    _check(lib().pql_moe_plan_workspace(T, k, n_experts, ctypes.byref(wsb)), "moe_plan")
+    if wsb.value and workspace is None:
+        workspace = torch.empty(wsb.value, dtype=torch.uint8, device=device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the ids' device")
+    P = T * k
+    buf = torch.empty(2 * P + n_experts + 1, dtype=torch.int32, device=device)   # one allocation for the three
+    plan = MoePlan(T, k, n_experts, buf[2 * P:], buf[:P], buf[P: 2 * P])
+    with _device_of(device):
+        _check(lib().pql_moe_plan(ids.data_ptr(), T, k, n_experts, plan.offsets.data_ptr(), plan.order.data_ptr(),
+                                  plan.slots.data_ptr(), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _stream(device)), "moe_plan")
+    return plan
+
+
+def moe_qgemm(a: QTensor, w: QTensor, plan: MoePlan, gather: bool = False,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each expert's product of its rows with its own weight: bf16 [T * top_k, N] in expert
+    order (rows from plan.offsets[-1] on are left as they were).
+
+    ``w`` is the quantized [n_experts * N, K] stack of the experts' weights.  ``gather``: ``a``
+    has one row per token, which its assignments share; otherwise one row per position."""
+    _check_qtensor(a, "a")
+    _check_qtensor(w, "w")
+    _check_plan(plan, w.device)
+    if a.role != "activation" or w.role != "weight":
+        raise ValueError("moe_qgemm takes a quantized activation and a quantized weight")
+    if a.scheme != w.scheme:
+        raise ValueError("activation and weight schemes differ")
+    _check_moe_scheme(w.scheme)
+    if a.device != w.device:
+        raise ValueError(f"activation on {a.device}, weight on {w.device}")
+    if a.cols != w.cols:
+        raise ValueError(f"K mismatch: {a.cols} vs {w.cols}")
+    if w.rows % plan.n_experts:
+        raise ValueError(f"{w.rows} weight rows do not divide into {plan.n_experts} experts")
+    P, N = plan.tokens * plan.top_k, w.rows // plan.n_experts
+    if a.rows != (plan.tokens if gather else P):
+        raise ValueError(f"expected an activation of {plan.tokens if gather else P} rows, got {a.rows}")
+    if out is None:
+        out = torch.empty((P, N), dtype=torch.bfloat16, device=w.device)
+    _check_out(out, P, N, w.device)
+    _on_device(w.device)
+    with _device_of(w.device):
+        _check(lib().pql_moe_qgemm(_scheme(w.scheme), a.codes.data_ptr(), a.scales.data_ptr(), a.rows, int(gather),
+                                   w.codes.data_ptr(), w.scales.data_ptr(), plan.offsets.data_ptr(),
+                                   plan.order.data_ptr(), plan.tokens, plan.top_k, plan.n_experts, N, w.cols,
+                                   out.data_ptr(), out.stride(0) if P > 1 else N, _stream(w.device)), "moe_qgemm")
+    return out
+
+
+def moe_kernel_name(scheme, T: int, top_k: int, n_experts: int, N: int, K: int) -> str:
+    return lib().pql_moe_kernel_name(_scheme(scheme), T, top_k, n_experts, N, K).decode()
+
+
+def swiglu_quantize(x: torch.Tensor, scheme: str, plan: MoePlan | None = None, out: QTensor | None = None) -> QTensor:
+    """silu(gate) * up of a bf16 [rows, 2 F] tensor (gate half first), quantized as a [rows, F]
+    activation in the same pass.  With ``plan`` the rows from plan.offsets[-1] on are left as
+    they were.  ``out`` reuses the buffers of an earlier result of the same shape."""
+    x = _as_2d_bf16(x)
+    _check_moe_scheme(scheme)
+    rows, cols = x.shape[0], x.shape[1] // 2
+    if x.shape[1] != 2 * cols:
+        raise ValueError("expected gate and up halves of equal width")
+    if plan is not None:
+        _check_plan(plan, x.device)
+        if rows != plan.tokens * plan.top_k:
+            raise ValueError(f"expected the plan's {plan.tokens * plan.top_k} rows, got {rows}")
+    if out is not None:
+        _check_qtensor(out, "out")
+        if (out.scheme, out.role, out.rows, out.cols) != (scheme, "activation", rows, cols):
+            raise ValueError("out does not match the scheme, role and shape")
+        if out.device != x.device:
+            raise ValueError(f"out is on {out.device}, x on {x.device}")
+        q = out
+    else:
+        q = _alloc_q(scheme, "activation", rows, cols, x.device)
+    with _device_of(x.device):
+        _check(lib().pql_swiglu_quantize(_scheme(scheme), x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else 2 * cols,
+                                         None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_experts,
+                                         q.codes.data_ptr(), q.scales.data_ptr(), _stream(x.device)),
+               "swiglu_quantize")
+    return q
+
+
+def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor, add: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Back to tokens: out[t] = add[t] + sum_j weights[t, j] * y[slot of (t, j)], bf16 [T, N],
+    summed in fp32.  ``add`` (a shared expert's output, a residual) may be ``out`` itself."""
+    _check_plan(plan)
+    T, P, device = plan.tokens, plan.tokens * plan.top_k, plan.device
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        raise ValueError("y must be a 2-D tensor")
+    N = y.shape[1]
+    _check_out(y, P, N, device, "y")
+    _check_vector(weights, "weights", torch.float32, P, device)
+    if add is not None:
+        _check_out(add, T, N, device, "add")
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=device)
+    _check_out(out, T, N, device)
+    _on_device(device)
+
+    def ld(t):
+        return t.stride(0) if t.shape[0] > 1 else N
+
+    with _device_of(device):
+        _check(lib().pql_moe_combine(y.data_ptr(), P, ld(y), plan.slots.data_ptr(), weights.data_ptr(), T, plan.top_k,
+                                     N, _ptr(add), N if add is None else ld(add), out.data_ptr(), ld(out),
+                                     _stream(device)), "moe_combine")
+    return out
+
+
+def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w_in: QTensor, w_out: QTensor,
+            n_experts: int, add: torch.Tensor | None = None) -> torch.Tensor:
+    """A layer of gated experts on bf16 x [T, K]: plan, quantize, product with ``w_in``
+    ([n_experts * 2 F, K]: gate rows, then up rows, of each expert), gated activation with its
+    quantization, product with ``w_out`` ([n_experts * N, F]), weighted sum to [T, N]."""
+    x = _as_2d_bf16(x)
+    _check_qtensor(w_in, "w_in")
+    _check_qtensor(w_out, "w_out")
+    _check_moe_scheme(w_in.scheme)
+    if w_in.scheme != w_out.scheme:
+        raise ValueError("the two weights' schemes differ")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError(f"ids must be [{x.shape[0]}, top_k]")
+    plan = moe_plan(ids, n_experts)
+    h = moe_qgemm(quantize(x, w_in.scheme), w_in, plan, gather=True)
+    y = moe_qgemm(swiglu_quantize(h, w_in.scheme, plan), w_out, plan)
+    return moe_combine(y, plan, weights, add=add)

@@ -770,3 +770,289 @@ const char* pql_kernel_name(int op, int scheme, int role, int64_t M, int64_t N, 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- experts
+// Mixture-of-experts entry points: route, plan, grouped GEMM, gated quantize, combine.
+namespace {
+
+// One line of the launch log for a call that is not described by M, N and K alone.
+void log_moe(pql_status st, const char* call, const std::string& shape, bool empty, const char* kernel,
+             const void* stream) {
+  if (st != PQL_OK)
+    std::fprintf(stderr, "[pql] %s %s: rejected (status %d): %s\n", call, shape.c_str(), (int)st, g_error.c_str());
+  else if (empty)
+    std::fprintf(stderr, "[pql] %s %s: nothing to do\n", call, shape.c_str());
+  else
+    std::fprintf(stderr, "[pql] %s %s -> %s on stream %p\n", call, shape.c_str(), kernel, stream);
+}
+
+std::string shape_text(const char* fmt, ...) {
+  char buf[160];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return buf;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// T tokens with k experts each out of E.
+pql_status check_assignments(int64_t T, int64_t k, int64_t E) {
+  if (T < 0) return fail(PQL_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %lld)", (long long)T);
+  if (E < 1 || E > pql::kMoeMaxExperts)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "E must be 1 .. %d (got %lld)", pql::kMoeMaxExperts, (long long)E);
+  if (k < 1 || k > pql::kMoeMaxTopK)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "k must be 1 .. %d (got %lld)", pql::kMoeMaxTopK, (long long)k);
+  if (T > pql::kMoeMaxRows / k)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "T * k above 2^24 - 1 is not supported (got %lld * %lld)", (long long)T,
+                (long long)k);
+  return PQL_OK;
+}
+
+// The schemes of the grouped GEMM and the gated quantize.
+pql_status check_moe_scheme(int scheme) {
+  if (!valid_scheme(scheme)) return fail(PQL_ERR_UNSUPPORTED, "unknown scheme %d", scheme);
+  if (scheme != PQL_FP8_ROW && scheme != PQL_FP8_BLOCK128)
+    return fail(PQL_ERR_UNSUPPORTED, "defined for FP8_ROW and FP8_BLOCK128 only (got %s)", scheme_name(scheme));
+  return PQL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+static pql_status moe_route_impl(int score, int dtype, const void* logits, int64_t T, int64_t E, int64_t ldl,
+                                 const float* bias, int64_t k, int64_t groups, int64_t top_groups, int group_score,
+                                 int renormalize, float scale, int32_t* ids, float* weights, void* stream) {
+  if (score != PQL_MOE_SOFTMAX && score != PQL_MOE_SIGMOID)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "unknown score %d", score);
+  if (dtype != PQL_F32 && dtype != PQL_BF16 && dtype != PQL_F16)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "unknown logits type %d", dtype);
+  if (group_score != PQL_MOE_GROUP_MAX && group_score != PQL_MOE_GROUP_TOP2)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "unknown group score %d", group_score);
+  pql_status st = check_assignments(T, k, E);
+  if (st != PQL_OK) return st;
+  if (groups < 1 || groups > pql::kMoeMaxGroups || E % groups)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "groups must be 1 .. %d and divide E = %lld (got %lld)", pql::kMoeMaxGroups,
+                (long long)E, (long long)groups);
+  if (top_groups < 1 || top_groups > groups)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "top_groups must be 1 .. groups = %lld (got %lld)", (long long)groups,
+                (long long)top_groups);
+  if (k > E / groups * top_groups)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "k = %lld is more than the %lld experts of %lld groups", (long long)k,
+                (long long)(E / groups * top_groups), (long long)top_groups);
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(PQL_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if ((st = check_ld("ldl", ldl, T, E, false)) != PQL_OK) return st;
+  if (T == 0) return ok();
+  if (!logits || !ids || !weights) return fail(PQL_ERR_INVALID_ARGUMENT, "logits, ids and weights must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(logits) & (dtype == PQL_F32 ? 3u : 1u)) || (bias && !aligned4(bias)) ||
+      !aligned4(ids) || !aligned4(weights))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "logits, bias, ids and weights must be aligned to their elements");
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::RouteArgs r{};
+  r.logits = logits;
+  r.T = T;
+  r.ldl = ldl;
+  r.E = (int)E;
+  r.k = (int)k;
+  r.score = score;
+  r.bias = bias;
+  r.groups = (int)groups;
+  r.top_groups = (int)top_groups;
+  r.group_score = group_score;
+  r.renormalize = renormalize != 0;
+  r.scale = scale;
+  r.ids = ids;
+  r.weights = weights;
+  return launched(pql::launch_moe_route(dtype, r, static_cast<hipStream_t>(stream)), "moe_route launch");
+}
+
+pql_status pql_moe_route(int score, int dtype, const void* logits, int64_t T, int64_t E, int64_t ldl,
+                         const float* bias, int64_t k, int64_t groups, int64_t top_groups, int group_score,
+                         int renormalize, float scale, int32_t* ids, float* weights, void* stream) {
+  const pql_status st = moe_route_impl(score, dtype, logits, T, E, ldl, bias, k, groups, top_groups, group_score,
+                                       renormalize, scale, ids, weights, stream);
+  if (log_enabled())
+    log_moe(st, "moe_route", shape_text("T=%lld E=%lld k=%lld", (long long)T, (long long)E, (long long)k), T == 0,
+            "k_moe_route", stream);
+  return st;
+}
+
+pql_status pql_moe_plan_workspace(int64_t T, int64_t k, int64_t E, size_t* bytes) {
+  if (!bytes) return fail(PQL_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  *bytes = 0;
+  const pql_status st = check_assignments(T, k, E);
+  if (st != PQL_OK) return st;
+  *bytes = pql::moe_plan_ws_bytes(T * k, (int)E);
+  return ok();
+}
+
+static pql_status moe_plan_impl(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offsets, int32_t* order,
+                                int32_t* slots, void* workspace, size_t workspace_bytes, void* stream) {
+  pql_status st = check_assignments(T, k, E);
+  if (st != PQL_OK) return st;
+  if (!offsets || (T > 0 && (!ids || !order || !slots)))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "ids, offsets, order and slots must be non-NULL");
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(order) || !aligned4(slots))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "ids, offsets, order and slots must be 4-byte aligned");
+  const size_t need = pql::moe_plan_ws_bytes(T * k, (int)E);
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(PQL_ERR_WORKSPACE, "moe_plan needs a %zu-byte workspace (got %zu)", need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(PQL_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  }
+  if ((st = check_device()) != PQL_OK) return st;
+  return launched(pql::launch_moe_plan(ids, T * k, (int)E, offsets, order, slots, static_cast<int32_t*>(workspace),
+                                       static_cast<hipStream_t>(stream)),
+                  "moe_plan launch");
+}
+
+pql_status pql_moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* offsets, int32_t* order,
+                        int32_t* slots, void* workspace, size_t workspace_bytes, void* stream) {
+  const pql_status st = moe_plan_impl(ids, T, k, E, offsets, order, slots, workspace, workspace_bytes, stream);
+  if (log_enabled())
+    log_moe(st, "moe_plan", shape_text("T=%lld k=%lld E=%lld", (long long)T, (long long)k, (long long)E), false,
+            st == PQL_OK ? pql::moe_plan_kernel_name(T * k, (int)E) : "", stream);
+  return st;
+}
+
+static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,
+                                 const void* w_codes, const void* w_scales, const int32_t* offsets,
+                                 const int32_t* order, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, void* c,
+                                 int64_t ldc, void* stream) {
+  pql_status st = check_moe_scheme(scheme);
+  if (st != PQL_OK) return st;
+  if ((st = check_assignments(T, k, E)) != PQL_OK) return st;
+  const int64_t P = T * k;
+  if ((st = check_gemm_shape(scheme, P, N, K)) != PQL_OK) return st;
+  if (N > (int64_t(1) << 20)) return fail(PQL_ERR_INVALID_ARGUMENT, "N above 2^20 is not supported");
+  if (E * N > (kMaxSpan / K)) return fail(PQL_ERR_INVALID_ARGUMENT, "an E x N x K weight of %lld x %lld x %lld is too large",
+                                          (long long)E, (long long)N, (long long)K);
+  if ((st = check_ld("ldc", ldc, P, N, false)) != PQL_OK) return st;
+  const int64_t want = gather ? T : P;
+  if (a_rows != want)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "the activation must have %s = %lld rows (got %lld)",
+                gather ? "T" : "T * k", (long long)want, (long long)a_rows);
+  if (P == 0) return ok();
+  if (!a || !a_scales || !w_codes || !w_scales || !offsets || !c || (gather && !order))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "operands, scales, offsets, order (to gather) and c must be non-NULL");
+  if (!aligned16(a) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "operands and scales must be 16-byte aligned");
+  if (!aligned4(offsets) || !aligned4(order) || (reinterpret_cast<uintptr_t>(c) & 1u))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "offsets, order and c must be aligned to their elements");
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::MoeGemmArgs g{};
+  g.a = static_cast<const uint8_t*>(a);
+  g.a_scales = static_cast<const float*>(a_scales);
+  g.a_rows = a_rows;
+  g.gather = gather != 0;
+  g.top_k = (int)k;
+  g.w = static_cast<const uint8_t*>(w_codes);
+  g.w_scales = static_cast<const float*>(w_scales);
+  g.offsets = offsets;
+  g.order = order;
+  g.P = (int)P;
+  g.E = (int)E;
+  g.N = N;
+  g.K = K;
+  g.c = static_cast<uint16_t*>(c);
+  g.ldc = ldc;
+  return launched(pql::launch_moe_gemm(scheme == PQL_FP8_ROW, g, static_cast<hipStream_t>(stream)), "moe_qgemm launch");
+}
+
+const char* pql_moe_kernel_name(int scheme, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+  if ((scheme != PQL_FP8_ROW && scheme != PQL_FP8_BLOCK128) || T < 1 || T > pql::kMoeMaxRows || k < 1 ||
+      k > pql::kMoeMaxTopK || E < 1 || E > pql::kMoeMaxExperts || N < 1 || K < 1)
+    return "";
+  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, T * k, E, N, K);
+}
+
+pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,
+                         const void* w_codes, const void* w_scales, const int32_t* offsets, const int32_t* order,
+                         int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, void* c, int64_t ldc, void* stream) {
+  const pql_status st = moe_qgemm_impl(scheme, a, a_scales, a_rows, gather, w_codes, w_scales, offsets, order, T, k, E,
+                                       N, K, c, ldc, stream);
+  if (log_enabled())
+    log_moe(st, "moe_qgemm",
+            shape_text("%s T=%lld k=%lld E=%lld N=%lld K=%lld", scheme_name(scheme), (long long)T, (long long)k,
+                       (long long)E, (long long)N, (long long)K),
+            T == 0, pql_moe_kernel_name(scheme, T, k, E, N, K), stream);
+  return st;
+}
+
+static pql_status swiglu_quantize_impl(int scheme, const void* x, int64_t rows, int64_t cols, int64_t ldx,
+                                       const int32_t* row_count, void* codes, void* scales, void* stream) {
+  pql_status st = check_moe_scheme(scheme);
+  if (st != PQL_OK) return st;
+  if ((st = check_shape(scheme, PQL_ACTIVATION, rows, cols)) != PQL_OK) return st;
+  if (rows > pql::kMoeMaxRows) return fail(PQL_ERR_INVALID_ARGUMENT, "rows above 2^24 - 1 is not supported");
+  if ((st = check_ld("ldx", ldx, rows, 2 * cols, true)) != PQL_OK) return st;
+  if (rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(PQL_ERR_INVALID_ARGUMENT, "x, codes and scales must be non-NULL");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned4(row_count))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "x, codes and scales must be 16-byte aligned, row_count 4-byte aligned");
+  if ((st = check_device()) != PQL_OK) return st;
+  return launched(pql::launch_swiglu_quantize(scheme == PQL_FP8_ROW, static_cast<const uint16_t*>(x), rows, cols, ldx,
+                                              row_count, static_cast<uint8_t*>(codes), static_cast<float*>(scales),
+                                              static_cast<hipStream_t>(stream)),
+                  "swiglu_quantize launch");
+}
+
+pql_status pql_swiglu_quantize(int scheme, const void* x, int64_t rows, int64_t cols, int64_t ldx,
+                               const int32_t* row_count, void* codes, void* scales, void* stream) {
+  const pql_status st = swiglu_quantize_impl(scheme, x, rows, cols, ldx, row_count, codes, scales, stream);
+  if (log_enabled())
+    log_call(st, "swiglu_quantize", scheme, PQL_ACTIVATION, rows, 0, cols,
+             scheme == PQL_FP8_ROW ? "k_swiglu_row" : "k_swiglu_block", stream);
+  return st;
+}
+
+static pql_status moe_combine_impl(const void* y, int64_t y_rows, int64_t ldy, const int32_t* slots,
+                                   const float* weights, int64_t T, int64_t k, int64_t N, const void* add,
+                                   int64_t ldadd, void* out, int64_t ldo, void* stream) {
+  pql_status st = check_assignments(T, k, 1);
+  if (st != PQL_OK) return st;
+  if (N < 1 || N > (int64_t(1) << 20)) return fail(PQL_ERR_INVALID_ARGUMENT, "N must be 1 .. 2^20 (got %lld)", (long long)N);
+  if (y_rows < 0 || y_rows > pql::kMoeMaxRows)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "y_rows must be 0 .. 2^24 - 1 (got %lld)", (long long)y_rows);
+  if ((st = check_ld("ldy", ldy, y_rows, N, false)) != PQL_OK) return st;
+  if (add && (st = check_ld("ldadd", ldadd, T, N, false)) != PQL_OK) return st;
+  if ((st = check_ld("ldo", ldo, T, N, false)) != PQL_OK) return st;
+  if (T == 0) return ok();
+  if ((y_rows > 0 && !y) || !slots || !weights || !out)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "y, slots, weights and out must be non-NULL");
+  if (!aligned4(slots) || !aligned4(weights) || ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(add) |
+                                                  reinterpret_cast<uintptr_t>(out)) & 1u))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "y, slots, weights, add and out must be aligned to their elements");
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::CombineArgs g{};
+  g.y = static_cast<const uint16_t*>(y);
+  g.P = y_rows;
+  g.ldy = ldy;
+  g.slots = slots;
+  g.weights = weights;
+  g.T = T;
+  g.k = (int)k;
+  g.N = N;
+  g.add = static_cast<const uint16_t*>(add);
+  g.ldadd = ldadd;
+  g.out = static_cast<uint16_t*>(out);
+  g.ldo = ldo;
+  const bool vec = N % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0 && (!add || ldadd % 8 == 0) && aligned16(y) &&
+                   aligned16(add) && aligned16(out);
+  return launched(pql::launch_moe_combine(g, vec, static_cast<hipStream_t>(stream)), "moe_combine launch");
+}
+
+pql_status pql_moe_combine(const void* y, int64_t y_rows, int64_t ldy, const int32_t* slots, const float* weights,
+                           int64_t T, int64_t k, int64_t N, const void* add, int64_t ldadd, void* out, int64_t ldo,
+                           void* stream) {
+  const pql_status st = moe_combine_impl(y, y_rows, ldy, slots, weights, T, k, N, add, ldadd, out, ldo, stream);
+  if (log_enabled())
+    log_moe(st, "moe_combine", shape_text("T=%lld k=%lld N=%lld", (long long)T, (long long)k, (long long)N), T == 0,
+            "k_moe_combine", stream);
+  return st;
+}
+
+}  // extern "C"

@@ -133,4 +133,66 @@ hipError_t launch_gemm_w4a16(const uint16_t* a, const uint32_t* wq, const uint16
                              uint16_t* c, int64_t ldc, hipStream_t st);
 const char* gemm_w4a16_kernel_name(int64_t M, int64_t N, int64_t K);
 
+// ---------------------------------------------------------------- experts
+struct RouteArgs {
+  const void* logits;      // [T, ldl]
+  int64_t T, ldl;
+  int E, k, score;         // score: 0 softmax, 1 sigmoid
+  const float* bias;       // fp32 [E] or null
+  int groups, top_groups, group_score;   // group_score: 0 best choice, 1 sum of the two best
+  int renormalize;
+  float scale;
+  int32_t* ids;            // [T, k]
+  float* weights;          // [T, k]
+};
+constexpr int kMoeMaxExperts = 1024, kMoeMaxTopK = 32, kMoeMaxGroups = 64;
+// Tokens, assignments and rows: a launch has at most 2^32 - 1 threads along an axis, and
+// some kernels give a row a workgroup of 256.
+constexpr int64_t kMoeMaxRows = (int64_t(1) << 24) - 1;
+// dtype of the logits: 0 fp32, 1 bf16, 2 fp16
+hipError_t launch_moe_route(int dtype, const RouteArgs& r, hipStream_t st);
+// Workspace of the grouping (0: none) and its launch; ws holds that many bytes.
+size_t moe_plan_ws_bytes(int64_t P, int E);
+const char* moe_plan_kernel_name(int64_t P, int E);
+hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* slots,
+                           int32_t* ws, hipStream_t st);
+
+struct MoeGemmArgs {
+  const uint8_t* a;        // activation codes [a_rows, K]
+  const float* a_scales;   // [a_rows, K / 128] or [a_rows]
+  int64_t a_rows;
+  int gather;              // row(p) = order[p] / top_k, else p
+  int top_k;
+  const uint8_t* w;        // weight codes [E, N, K]
+  const float* w_scales;   // [E, N / 128, K / 128] or [E, N]
+  const int32_t* offsets;  // [E + 1]
+  const int32_t* order;    // [P]
+  int P, E;
+  int64_t N, K;
+  uint16_t* c;             // bf16 [P, ldc]
+  int64_t ldc;
+};
+hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st);
+const char* moe_gemm_kernel_name(bool row_scales, int64_t P, int64_t E, int64_t N, int64_t K);
+
+// Codes and scales of silu(x[:, :F]) * x[:, F:]; rows at and past *count (if given) are left alone.
+hipError_t launch_swiglu_quantize(bool per_row, const uint16_t* x, int64_t rows, int64_t F, int64_t ldx,
+                                  const int32_t* count, uint8_t* codes, float* scales, hipStream_t st);
+
+struct CombineArgs {
+  const uint16_t* y;       // bf16 [P, ldy]
+  int64_t P, ldy;
+  const int32_t* slots;    // [T, k]
+  const float* weights;    // [T, k]
+  int64_t T;
+  int k;
+  int64_t N;
+  const uint16_t* add;     // bf16 [T, ldadd] or null
+  int64_t ldadd;
+  uint16_t* out;           // bf16 [T, ldo]
+  int64_t ldo;
+};
+// vec: every row of y, add and out starts on 16 bytes and N % 8 == 0
+hipError_t launch_moe_combine(const CombineArgs& g, bool vec, hipStream_t st);
+
 }  // namespace pql

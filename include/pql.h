@@ -408,7 +408,7 @@ pql_status pql_moe_combine(const void* y, int64_t y_rows, int64_t ldy, const int
                            void* stream);
 
 /* Name of the kernel pql_moe_qgemm would launch; "" if the combination is invalid. */
-const char* pql_moe_kernel_name(int scheme, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }

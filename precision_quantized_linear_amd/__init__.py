@@ -65,7 +65,7 @@ def lib() -> ctypes.CDLL:
         L.pql_qlinear_noalloc.argtypes = [ci, vp, i64, i64, i64, vp, vp, vp, vp, i64, f32, vp, vp, i64, vp]
         L.pql_noalloc_scratch_bytes.restype = sz
         L.pql_moe_kernel_name.restype = ctypes.c_char_p
-        L.pql_moe_kernel_name.argtypes = [ci, i64, i64, i64, i64, i64]
+        L.pql_moe_kernel_name.argtypes = [ci, ci, i64, i64, i64, i64, i64]
         L.pql_moe_route.argtypes = [ci, ci, vp, i64, i64, i64, vp, i64, i64, i64, ci, ci, f32, vp, vp, vp]
         L.pql_moe_plan_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
         L.pql_moe_plan.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
@@ -687,8 +687,8 @@ def moe_qgemm(a: QTensor, w: QTensor, plan: MoePlan, gather: bool = False,
     return out
 
 
-def moe_kernel_name(scheme, T: int, top_k: int, n_experts: int, N: int, K: int) -> str:
-    return lib().pql_moe_kernel_name(_scheme(scheme), T, top_k, n_experts, N, K).decode()
+def moe_kernel_name(scheme, T: int, top_k: int, n_experts: int, N: int, K: int, gather: bool = False) -> str:
+    return lib().pql_moe_kernel_name(_scheme(scheme), int(gather), T, top_k, n_experts, N, K).decode()
 
 
 def swiglu_quantize(x: torch.Tensor, scheme: str, plan: MoePlan | None = None, out: QTensor | None = None) -> QTensor:

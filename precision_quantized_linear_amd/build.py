@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpql.so")
 SOURCES = ("abi.cpp", "quant.hip", "layout.hip", "gemm.hip", "gemm32.hip", "gemm_block.hip", "gemm_block256.hip", "gemm_w4a16.hip", "gemm_dual.hip", "qlinear_small.hip",
-           "gemm_w4a16_mm.hip", "moe_route.hip", "moe_gemm.hip", "moe_ffn.hip")
+           "gemm_w4a16_mm.hip", "moe_route.hip", "moe_gemm.hip",
+           "moe_gemm_tile.hip", "moe_ffn.hip")
 ARCH = "gfx950"
 
 
@@ -42,7 +43,8 @@ def compile_flags():
 # partial product with VALU FMAs; taking the MFMA results in VGPRs (instead of
 # AGPRs) spares one v_accvgpr_read per element.
 EXTRA_FLAGS = {"gemm_block.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "gemm_block256.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "gemm_block256.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "moe_gemm_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

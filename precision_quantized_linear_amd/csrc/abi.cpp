@@ -959,14 +959,15 @@ static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales
   g.K = K;
   g.c = static_cast<uint16_t*>(c);
   g.ldc = ldc;
+  g.vec_store = aligned16(c) && ldc % 8 == 0;
   return launched(pql::launch_moe_gemm(scheme == PQL_FP8_ROW, g, static_cast<hipStream_t>(stream)), "moe_qgemm launch");
 }
 
-const char* pql_moe_kernel_name(int scheme, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
   if ((scheme != PQL_FP8_ROW && scheme != PQL_FP8_BLOCK128) || T < 1 || T > pql::kMoeMaxRows || k < 1 ||
       k > pql::kMoeMaxTopK || E < 1 || E > pql::kMoeMaxExperts || N < 1 || K < 1)
     return "";
-  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, T * k, E, N, K);
+  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, gather != 0, T, k, E, K);
 }
 
 pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,
@@ -978,7 +979,7 @@ pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_
     log_moe(st, "moe_qgemm",
             shape_text("%s T=%lld k=%lld E=%lld N=%lld K=%lld", scheme_name(scheme), (long long)T, (long long)k,
                        (long long)E, (long long)N, (long long)K),
-            T == 0, pql_moe_kernel_name(scheme, T, k, E, N, K), stream);
+            T == 0, pql_moe_kernel_name(scheme, gather, T, k, E, N, K), stream);
   return st;
 }
 

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "gemm_common.hpp"
+#include "moe_gemm.hpp"
 #include "pql_device.hpp"
 #include "pql_internal.hpp"
 
@@ -26,18 +27,6 @@ constexpr int kBatch = 3;
 constexpr int kCols = 32;
 
 typedef float v4f_t __attribute__((ext_vector_type(4)));
-
-// Expert e's assignments, inside 0 .. P whatever the offsets hold.
-__device__ __forceinline__ void expert_range(const MoeGemmArgs& g, int e, int& lo, int& hi) {
-  lo = std::min(std::max(g.offsets[e], 0), g.P);
-  hi = std::min(std::max(g.offsets[e + 1], lo), g.P);
-}
-
-// The activation row of assignment p (clamped into the operand).
-__device__ __forceinline__ int64_t a_row(const MoeGemmArgs& g, int p) {
-  const int64_t r = g.gather ? (int64_t)((uint32_t)std::max(g.order[p], 0) / (uint32_t)g.top_k) : (int64_t)p;
-  return std::min<int64_t>(r, g.a_rows - 1);
-}
 
 template <bool ROW>
 __global__ __launch_bounds__(kThreads) void k_moe_stream(MoeGemmArgs g) {
@@ -127,15 +116,30 @@ __global__ __launch_bounds__(kThreads) void k_moe_stream(MoeGemmArgs g) {
 
 }  // namespace
 
+// Rows per tile, or 0 for the streaming kernel.
+static int tile_rows(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t K) {
+  // gathered rows are addressed with 32-bit offsets from the activation's start
+  if (gather && a_rows * K > int64_t(0xFFFF0000)) return 0;
+  const int64_t per = P / E;   // rows per expert, were they spread evenly
+  if (per < 24) return 0;
+  return per < 96 ? 64 : per < 384 ? 128 : 256;
+}
+
 hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st) {
+  const int bm = tile_rows(g.P, g.E, g.gather, g.a_rows, g.K);
+  if (bm) return launch_moe_tile(row_scales, bm, g, st);
   const dim3 grid((unsigned)((g.N + kCols - 1) / kCols), (unsigned)g.E);
   if (row_scales) hipLaunchKernelGGL(k_moe_stream<true>, grid, dim3(kThreads), 0, st, g);
   else hipLaunchKernelGGL(k_moe_stream<false>, grid, dim3(kThreads), 0, st, g);
   return hipGetLastError();
 }
 
-const char* moe_gemm_kernel_name(bool row_scales, int64_t P, int64_t E, int64_t N, int64_t K) {
-  (void)P; (void)E; (void)N; (void)K;
+const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t K) {
+  switch (tile_rows(T * k, E, gather, gather ? T : T * k, K)) {
+    case 64: return row_scales ? "k_moe_tile<64, fp8_row>" : "k_moe_tile<64, fp8_block128>";
+    case 128: return row_scales ? "k_moe_tile<128, fp8_row>" : "k_moe_tile<128, fp8_block128>";
+    case 256: return row_scales ? "k_moe_tile<256, fp8_row>" : "k_moe_tile<256, fp8_block128>";
+  }
   return row_scales ? "k_moe_stream<fp8_row>" : "k_moe_stream<fp8_block128>";
 }
 

@@ -1,0 +1,408 @@
+// Grouped FP8 products for experts with many rows, gfx950 (tiles of BM rows by 256 columns).
+//
+// The mathematics is moe_gemm.hip's.  A tile belongs to one expert: BM = 64, 128 or 256 of its
+// rows and 256 of its columns.  8 waves, two per SIMD, as 2 x 4: wave w owns the (BM / 2) x 64
+// part (w / 4, w % 4), as MI x 2 blocks of v_mfma_scale_f32_32x32x64_f8f6f4 with unit scales,
+// the W fragment first, so lane l of a block holds row l % 32 and four quads of consecutive
+// columns.  FP8_BLOCK128: a K-group's partial product is promoted into the fp32 sums with one
+// FMA per element while the SIMD's other wave runs its MFMAs; FP8_ROW: the matrix core
+// accumulates over all of K and the scales come in the epilogue.
+//
+// Pipeline: LDS holds S K-groups ("regions": BM activation rows and 256 weight rows of 128
+// bytes, each row's 16-byte chunk c at c ^ ((r / 2) % 8), and the group's scales), S = 2 for
+// BM = 256 and 3 below.  At the start of region R every wave waits for its own loads of R and
+// meets the others at a barrier; the slot of region R - 1 is then free and each wave issues its
+// share of region R + S - 1 into it, direct to LDS.  The load stream runs ahead over tile
+// boundaries with a cursor of its own.
+//
+// Gathered rows cost nothing extra in the stream: each lane's row offset within the activation
+// is formed once per tile from the plan's order and every load adds the K offset in the scalar
+// operand.  Rows past the expert's last read zero (their offset lies outside the descriptor).
+//
+// Schedule: persistent, one workgroup per CU.  Tile counts per expert come from the plan's
+// offsets (on the device: the host never learns them); every workgroup sums them into a prefix
+// in LDS, and takes tiles XCD by XCD, expert by expert, in 4-tile-tall column walks, so that
+// workgroups of an XCD share an expert's weight rows in its L2.
+#include <algorithm>
+
+#include "gemm_common.hpp"
+#include "moe_gemm.hpp"
+#include "pql_device.hpp"
+#include "pql_internal.hpp"
+
+namespace pql {
+
+namespace {
+
+using namespace gemm;
+
+constexpr int kThreads = 512;
+constexpr int kWaves = 8;
+constexpr int BN = 256;
+constexpr int kRow = 128;                          // bytes of one K-group per row
+constexpr int kEpiBytes = 8 * 128;                 // per wave: 8 staged output rows of 64 bf16
+constexpr int kPersistentCap = 256;
+constexpr uint32_t kOutside = 0xFFFFFFF0u;         // a row offset outside every descriptor
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+template <int MI, bool ROW>
+struct Shape {
+  static constexpr int BM = 64 * MI;
+  static constexpr int kAOp = BM * kRow;
+  static constexpr int kRegion = kAOp + BN * kRow;
+  static constexpr int kSlots = MI == 4 ? 2 : 3;
+  static constexpr int kSaBytes = ROW ? 0 : BM * 4;        // activation scales of one group
+  static constexpr int kSwBytes = ROW ? 0 : 256;           // a weight block's scale, one copy per lane
+  static constexpr int kScales = kSlots * kRegion;
+  static constexpr int kEpi = kScales + kSlots * (kSaBytes + 2 * kSwBytes);
+  static constexpr int kPrefix = kEpi + kWaves * kEpiBytes;
+  static constexpr int kLds = kPrefix + 4 * (kMoeMaxExperts + 4);
+  static_assert(kLds <= 160 * 1024, "a CU has 160 KB of LDS");
+};
+
+template <int MI, bool ROW>
+__global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
+  using S = Shape<MI, ROW>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int Kb = (int)g.K;
+  const int G = Kb / kRow;                         // K-groups = regions per tile
+  const int tiles_n = (int)((g.N + BN - 1) / BN);
+  const int nblocks = (int)(g.N / 128);            // weight-scale blocks along N (block-128)
+
+  // ---- row tiles before each expert: prefix[e], prefix[E] = all of them
+  int* const prefix = reinterpret_cast<int*>(smem + S::kPrefix);
+  if (wave == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int e = e0 + lane;
+      int lo = 0, hi = 0;
+      if (e < g.E) expert_range(g, e, lo, hi);
+      const int n = (hi - lo + S::BM - 1) / S::BM;
+      int s = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(s, o);
+        if (lane >= o) s += u;
+      }
+      if (e < g.E) prefix[e] = carry + s - n;
+      carry += __shfl(s, 63);
+    }
+    // a plan has at most P / BM + E row tiles; wild offsets are cut there
+    if (lane == 0) prefix[g.E] = std::min(carry, g.P / S::BM + g.E);
+  }
+  __syncthreads();
+  const int row_tiles = __builtin_amdgcn_readfirstlane(prefix[g.E]);
+  Sched sched;
+  sched.init(row_tiles * tiles_n, row_tiles, tiles_n);
+  const int my_tiles = __builtin_amdgcn_readfirstlane(sched.count);
+  if (my_tiles == 0) return;
+
+  // Tile k of this workgroup: its expert, first row, first column and the end of the expert's rows.
+  struct Tile {
+    int e, m0, hi, n0;
+  };
+  auto tile_at = [&](int k) __attribute__((always_inline)) {
+    const int L = sched.first + k * sched.stride;
+    int e = -1;   // the last expert whose tiles start at or before L
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int i = std::min(e0 + lane, g.E);
+      const uint64_t before = __ballot(e0 + lane < g.E && prefix[i] * tiles_n <= L);
+      e += __popcll(before);
+      if (before != ~uint64_t(0)) break;
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int first = __builtin_amdgcn_readfirstlane(prefix[e]);
+    int lo, hi;
+    expert_range(g, e, lo, hi);
+    const int tiles_m = (hi - lo + S::BM - 1) / S::BM;
+    const int l = L - first * tiles_n;
+    constexpr int kGroupM = 4;
+    const int group = l / (kGroupM * tiles_n);
+    const int first_m = group * kGroupM;
+    const int gm = std::max(1, std::min(tiles_m - first_m, kGroupM));
+    const int r = l - group * kGroupM * tiles_n;
+    Tile tl;
+    tl.e = e;
+    tl.m0 = __builtin_amdgcn_readfirstlane(lo + (first_m + r % gm) * S::BM);
+    tl.hi = __builtin_amdgcn_readfirstlane(hi);
+    tl.n0 = __builtin_amdgcn_readfirstlane((r / gm) * BN);
+    return tl;
+  };
+
+  // ---- load stream (see the file comment).  Load p of a wave covers activation rows
+  // 8 MI w + 8 p .. + 7 and weight rows 32 w + 8 p .. + 7 of the tile, whole 128-byte lines.
+  int voff_w[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) voff_w[p] = (wave * 32 + 8 * p + (lane >> 3)) * Kb + (dma_chunk(lane, p & 1) << 4);
+  struct Cursor {
+    v4i a, w, sa, sw;   // descriptors of the tile's codes and scales
+    uint32_t voff_a[MI];
+    uint32_t voff_sa;
+    int k, rg;          // tile, region within it
+  } cur;
+  // block-128: waves 0 .. MI - 1 load the activation scales of 64 rows each, waves 4 and 6 the
+  // weight scales of the tile's two 128-column blocks
+  const bool sa_wave = !ROW && wave < MI, sw_wave = !ROW && (wave == 4 || wave == 6);
+  auto cursor_tile = [&](int k) __attribute__((always_inline)) {
+    const Tile tl = tile_at(std::min(k, my_tiles - 1));
+    const int64_t base = g.gather ? 0 : (int64_t)tl.m0;   // gathered rows are offset from the operand's start
+    const uint64_t rows = g.gather ? (uint64_t)g.a_rows : (uint64_t)std::min(S::BM, tl.hi - tl.m0);
+    auto row_of = [&](int m) __attribute__((always_inline)) {   // the row (from base) of tile row m, inside the operand
+      if (!g.gather) return (uint32_t)m;
+      const uint32_t tok = (uint32_t)std::max(g.order[std::min(tl.m0 + m, tl.hi - 1)], 0) / (uint32_t)g.top_k;
+      return std::min<uint32_t>(tok, (uint32_t)g.a_rows - 1);
+    };
+    const int live = tl.hi - tl.m0;
+#pragma unroll
+    for (int p = 0; p < MI; ++p) {
+      const int m = wave * 8 * MI + 8 * p + (lane >> 3);
+      const int odd = MI == 1 ? (wave & 1) : (p & 1);   // parity of the 8-row group
+      cur.voff_a[p] = m < live ? row_of(m) * (uint32_t)Kb + (uint32_t)(dma_chunk(lane, odd) << 4) : kOutside;
+    }
+    const int64_t n = (int64_t)tl.e * g.N + tl.n0;
+    const int nr = (int)std::min<int64_t>(BN, g.N - tl.n0);
+    cur.a = make_rsrc(g.a + base * Kb, (int)(uint32_t)(rows * (uint64_t)Kb));
+    cur.w = make_rsrc(g.w + n * Kb, nr * Kb);
+    if constexpr (!ROW) {
+      const int m = (wave & (MI - 1)) * 64 + lane;
+      cur.voff_sa = m < live ? row_of(m) * (uint32_t)(G * 4) : kOutside;
+      // the wave's weight block; a wave wholly past N takes the last one (its sums are never stored)
+      const int nb = std::min(tl.n0 / 128 + (wn >> 1), nblocks - 1);
+      cur.sa = make_rsrc(g.a_scales + base * G, (int)(uint32_t)(rows * (uint64_t)(G * 4)));
+      cur.sw = make_rsrc(g.w_scales + ((int64_t)tl.e * nblocks + nb) * G, G * 4);
+    }
+    cur.k = k;
+    cur.rg = 0;
+  };
+  uint8_t* const sa_lds = smem + S::kScales;                            // [slot][BM] floats
+  uint8_t* const sw_lds = sa_lds + S::kSlots * S::kSaBytes;             // [slot][block][64] floats
+  uint8_t* const epi = smem + S::kEpi + wave * kEpiBytes;               // this wave's output staging
+  // Loads per wave and region, which the waits count: these, and one of scales on some waves.
+  constexpr int kLoads = MI + 4;
+  // The next region of the stream into `slot` (past the last tile: that tile again, into slots
+  // that are never read).
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    uint8_t* const base = smem + slot * S::kRegion;
+    const int so = cur.rg * kRow;
+    if constexpr (!ROW) {   // the scales first: a gather, one cache line per row
+      if (sa_wave) lds_load4_so(cur.sa, sa_lds + slot * S::kSaBytes + wave * 256, (int)cur.voff_sa, cur.rg * 4);
+      if (sw_wave) lds_load4_so(cur.sw, sw_lds + (slot * 2 + (wn >> 1)) * S::kSwBytes, 0, cur.rg * 4);
+    }
+#pragma unroll
+    for (int p = 0; p < MI; ++p)
+      lds_load16_so(cur.a, base + (wave * 8 * MI + 8 * p) * kRow, (int)cur.voff_a[p], so);
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      lds_load16_so(cur.w, base + S::kAOp + (wave * 32 + 8 * p) * kRow, voff_w[p], so);
+    if (++cur.rg == G) cursor_tile(cur.k + 1);
+  };
+
+  // ---- fragments: 32x32x64 operands, lane row l % 32; slice h takes chunks 4 h + c and
+  // 4 h + 2 + c (c = l / 32) of the row; rows + 32 i keep the swizzle.
+  const int r32 = lane & 31, c32 = lane >> 5;
+  int a_off[2][2], w_off[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      a_off[h][q] = swz128(wm * 32 * MI + r32, 4 * h + 2 * q + c32);
+      w_off[h][q] = S::kAOp + swz128(wn * 64 + r32, 4 * h + 2 * q + c32);
+    }
+  uint4 fw[2][2][2];   // [j][slice][chunk]
+  uint4 fa[2][2][2];   // [buffer][slice][chunk]: A block i in buffer i % 2
+  auto read_w = [&](const uint8_t* region) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) fw[j][h][q] = lds16(region + w_off[h][q] + j * 32 * kRow);
+  };
+  auto read_a = [&](const uint8_t* region, int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) fa[i & 1][h][q] = lds16(region + a_off[h][q] + i * 32 * kRow);
+  };
+  float sc[MI], last_sc = 0.f;   // s_a * s_w per 32-row block: this region's; the previous region's last
+  auto read_scales = [&](int slot) __attribute__((always_inline)) {
+    const float* sa = reinterpret_cast<const float*>(sa_lds + slot * S::kSaBytes) + wm * 32 * MI + r32;
+    const float sw = reinterpret_cast<const float*>(sw_lds + (slot * 2 + (wn >> 1)) * S::kSwBytes)[lane];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sc[i] = sa[i * 32] * sw;
+  };
+
+  v16f acc[MI][2];
+  v16f P[2];   // partial products of consecutive blocks, alternating (block-128)
+  auto promote = [&](int b, float s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[b >> 1][b & 1][e] = __builtin_fmaf(P[b & 1][e], s, acc[b >> 1][b & 1][e]);
+  };
+  auto region = [&](int slot, int next_slot, bool carry) __attribute__((always_inline)) {
+    const uint8_t* rgn = smem + slot * S::kRegion;
+    issue(next_slot);
+    read_w(rgn);
+    read_a(rgn, 0);
+    if constexpr (!ROW) {
+      if (carry) last_sc = sc[MI - 1];
+      read_scales(slot);
+      if (carry) promote(2 * MI - 1, last_sc);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < 2 * MI; ++b) {
+      const int i = b >> 1, j = b & 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v8i w8 = cat(fw[j][h][0], fw[j][h][1]), a8 = cat(fa[i & 1][h][0], fa[i & 1][h][1]);
+        if constexpr (ROW)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc[i][j], 0, 0, 0, 127, 0, 127);
+        else
+          P[b & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, h ? P[b & 1] : v16f{}, 0, 0, 0, 127, 0, 127);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (j == 0 && i + 1 < MI) read_a(rgn, i + 1);
+      if constexpr (!ROW) {
+        if (b > 0) promote(b - 1, sc[(b - 1) >> 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // ---- epilogue.  In block (i, j) lane (r, c) = (l % 32, l / 32) holds, per register quad rq,
+  // columns 8 rq + 4 c .. + 3 of row 32 i + r.  One v_permlane32_swap per packed dword leaves the
+  // lane 8 consecutive columns; where rows of C start on 16 bytes and the wave's 64 columns
+  // exist they are staged 8 rows at a time (16-byte piece c of row r at c ^ r) and written as
+  // whole 128-byte row segments.
+  auto epilogue = [&](int k) __attribute__((always_inline)) {
+    const Tile tl = tile_at(k);
+    const int m0 = tl.m0 + wm * 32 * MI;
+    const int64_t n0 = tl.n0 + wn * 64;
+    const bool staged = g.vec_store && n0 + 64 <= g.N;   // wave-uniform
+    const int el = fresh_lane();
+    const int fr = el & 31, fk = el >> 5;
+    const int rr = el >> 3, rc = el & 7;   // staged read-back: row rr, 16-byte piece rc
+    float cs[2][16];                       // FP8_ROW: the scales of the lane's columns
+    if constexpr (ROW) {
+      const float* sw = g.w_scales + (int64_t)tl.e * g.N;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) cs[j][q] = sw[std::min<int64_t>(n0 + j * 32 + (q >> 2) * 8 + fk * 4 + (q & 3), g.N - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (m0 + i * 32 >= tl.hi) break;     // wave-uniform
+      float rs = 1.0f;
+      if constexpr (ROW) rs = g.a_scales[a_row(g, std::min(m0 + i * 32 + fr, tl.hi - 1))];
+      uint4 u[2][2];   // [j][h]
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t d[4][2];
+#pragma unroll
+        for (int rq = 0; rq < 4; ++rq) {
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = ROW ? acc[i][j][4 * rq + q] * rs * cs[j][4 * rq + q] : acc[i][j][4 * rq + q];
+          d[rq][0] = pack_bf16x2(v[0], v[1]);
+          d[rq][1] = pack_bf16x2(v[2], v[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto s0 = __builtin_amdgcn_permlane32_swap(d[2 * h][0], d[2 * h + 1][0], false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(d[2 * h][1], d[2 * h + 1][1], false, false);
+          u[j][h] = uint4{s0[0], s1[0], s0[1], s1[1]};
+        }
+      }
+      if (staged) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {   // rows 8 p .. + 7 of the block
+          if ((fr >> 3) == p) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4*>(epi + (fr & 7) * 128 + (((j * 4 + h * 2 + fk) ^ (fr & 7)) << 4)) = u[j][h];
+          }
+          // rows pass between lanes of the wave (LDS runs one wave's accesses in order)
+          asm volatile("" ::: "memory");
+          const uint4 w = lds16(epi + rr * 128 + ((rc ^ rr) << 4));
+          asm volatile("" ::: "memory");
+          const int row = m0 + i * 32 + 8 * p + rr;
+          if (row < tl.hi) *reinterpret_cast<uint4*>(g.c + (int64_t)row * g.ldc + n0 + rc * 8) = w;
+        }
+      } else {
+        const int row = m0 + i * 32 + fr;
+        if (row < tl.hi) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int64_t col = n0 + j * 32 + h * 16 + 8 * fk;
+              uint16_t* dst = g.c + (int64_t)row * g.ldc + col;
+              const uint32_t wds[4] = {u[j][h].x, u[j][h].y, u[j][h].z, u[j][h].w};
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (col + c < g.N) dst[c] = (uint16_t)(wds[c >> 1] >> (16 * (c & 1)));
+            }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);   // one accumulator block at a time
+    }
+  };
+
+  // ---- the stream
+  cursor_tile(0);
+#pragma unroll
+  for (int s = 0; s < S::kSlots - 1; ++s) issue(s);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) sc[i] = 0.f;
+  int slot = 0;
+  for (int k = 0; k < my_tiles; ++k) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
+    for (int r = 0; r < G; ++r) {
+      // this wave's loads of the region (those of the S - 2 regions after it may be in flight)
+      if constexpr (S::kSlots == 2) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+      } else if (sa_wave || sw_wave) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * (kLoads + 1), 0));
+      } else {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * kLoads, 0));
+      }
+      __builtin_amdgcn_s_barrier();   // everyone's; the previous region's slot is free
+      __builtin_amdgcn_sched_barrier(0);
+      region(slot, slot == 0 ? S::kSlots - 1 : slot - 1, r > 0);
+      slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+    }
+    if constexpr (!ROW) promote(2 * MI - 1, sc[MI - 1]);   // the tile's last block
+    epilogue(k);
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+}
+
+template <int MI, bool ROW>
+hipError_t launch_shape(const MoeGemmArgs& g, hipStream_t st) {
+  constexpr int BM = 64 * MI;
+  const int64_t row_tiles = g.P / BM + std::min(g.P, g.E);
+  const int64_t tiles = row_tiles * ((g.N + BN - 1) / BN);
+  hipLaunchKernelGGL((k_moe_tile<MI, ROW>), dim3((unsigned)std::min<int64_t>(tiles, kPersistentCap)), dim3(kThreads), 0,
+                     st, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_tile(bool row_scales, int bm, const MoeGemmArgs& g, hipStream_t st) {
+  if (row_scales)
+    return bm == 64 ? launch_shape<1, true>(g, st) : bm == 128 ? launch_shape<2, true>(g, st) : launch_shape<4, true>(g, st);
+  return bm == 64 ? launch_shape<1, false>(g, st) : bm == 128 ? launch_shape<2, false>(g, st) : launch_shape<4, false>(g, st);
+}
+
+}  // namespace pql

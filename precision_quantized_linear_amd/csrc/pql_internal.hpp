@@ -171,9 +171,12 @@ struct MoeGemmArgs {
   int64_t N, K;
   uint16_t* c;             // bf16 [P, ldc]
   int64_t ldc;
+  int vec_store;           // 1 if c and ldc allow 16-byte row stores
 };
 hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st);
-const char* moe_gemm_kernel_name(bool row_scales, int64_t P, int64_t E, int64_t N, int64_t K);
+// Tiles of bm = 64, 128 or 256 rows (a gathered activation of at most 2^32 - 2^16 bytes).
+hipError_t launch_moe_tile(bool row_scales, int bm, const MoeGemmArgs& g, hipStream_t st);
+const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t K);
 
 // Codes and scales of silu(x[:, :F]) * x[:, F:]; rows at and past *count (if given) are left alone.
 hipError_t launch_swiglu_quantize(bool per_row, const uint16_t* x, int64_t rows, int64_t F, int64_t ldx,

@@ -12,6 +12,7 @@ There is no CPU fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -271,7 +272,7 @@ def _check_qtensor(q: QTensor, what: str) -> None:
 
 
 def _on_device(device) -> None:
-    if torch.device(device).type != "cuda":
+    if (device if isinstance(device, torch.device) else torch.device(device)).type != "cuda":
         raise ValueError(f"operands must be on a HIP device, not {device}")
 
 
@@ -551,21 +552,30 @@ class MoePlan:
         return self.offsets.device
 
 
-class _device_of:
-    """Make a tensor's device current for a launch; nothing where it already is."""
+def _call(fn, what: str, device, *args) -> None:
+    """One launch on the device's current stream, with that device current."""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)   # current_stream() without building a Stream object
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != PQL_OK:
+        _check(status, what)
 
-    def __init__(self, device):
-        self.index = device.index
-        self.guard = None
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _check_rows(t, name: str, rows: int, cols: int, device) -> int:
+    """The row stride of a bf16 [rows, cols] operand with unit column stride on ``device``."""
+    if type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.device == device and t.dim() == 2:
+        (r, c), (ld, unit) = t.shape, t.stride()
+        if r == rows and c == cols:
+            if rows <= 1 and (unit == 1 or cols == 1):
+                return cols
+            if unit == 1 and ld >= cols:
+                return ld
+    _check_out(t, rows, cols, device, name)   # names what is wrong
+    return t.stride(0) if rows > 1 else cols
 
 
 def _check_vector(t, name: str, dtype, n: int, device) -> None:
@@ -618,12 +628,17 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
     weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
     ld = logits.stride(0) if T > 1 else E
-    with _device_of(device):
-        _check(lib().pql_moe_route(MOE_SCORES[score], _LOGIT_TYPES[logits.dtype], logits.data_ptr(), T, E, ld,
-                                   _ptr(bias), k, n_groups, top_groups, MOE_GROUP_SCORES[group_score],
-                                   int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
-                                   _stream(device)), "moe_route")
+    _call(lib().pql_moe_route, "moe_route", device, MOE_SCORES[score], _LOGIT_TYPES[logits.dtype], logits.data_ptr(), T,
+          E, ld, _ptr(bias), k, n_groups, top_groups, MOE_GROUP_SCORES[group_score], bool(renormalize), scale,
+          ids.data_ptr(), weights.data_ptr())
     return ids, weights
+
+
+@functools.lru_cache(maxsize=None)
+def _plan_workspace(T: int, k: int, n_experts: int) -> int:
+    wsb = ctypes.c_size_t()
+    _check(lib().pql_moe_plan_workspace(T, k, n_experts, ctypes.byref(wsb)), "moe_plan")
+    return wsb.value
 
 
 def moe_plan(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | None = None) -> MoePlan:
@@ -634,20 +649,20 @@ def moe_plan(ids: torch.Tensor, n_experts: int, workspace: torch.Tensor | None =
     T, k = ids.shape
     device = ids.device
     _on_device(device)
-    wsb = ctypes.c_size_t()
-    _check(lib().pql_moe_plan_workspace(T, k, n_experts, ctypes.byref(wsb)), "moe_plan")
-    if wsb.value and workspace is None:
-        workspace = torch.empty(wsb.value, dtype=torch.uint8, device=device)
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on the ids' device")
+    wsb = _plan_workspace(T, k, n_experts)
     P = T * k
-    buf = torch.empty(2 * P + n_experts + 1, dtype=torch.int32, device=device)   # one allocation for the three
-    plan = MoePlan(T, k, n_experts, buf[2 * P:], buf[:P], buf[P: 2 * P])
-    with _device_of(device):
-        _check(lib().pql_moe_plan(ids.data_ptr(), T, k, n_experts, plan.offsets.data_ptr(), plan.order.data_ptr(),
-                                  plan.slots.data_ptr(), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                  _stream(device)), "moe_plan")
+    ws_at = (2 * P + n_experts + 1 + 3) // 4 * 4                 # one allocation for the plan and the workspace
+    buf = torch.empty(ws_at + (0 if workspace is not None else wsb // 4), dtype=torch.int32, device=device)
+    if workspace is None:
+        ws, wsn = buf.data_ptr() + 4 * ws_at, wsb
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the ids' device")
+        ws, wsn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    order, slots, offsets, _ = buf.split((P, P, n_experts + 1, buf.numel() - 2 * P - n_experts - 1))
+    plan = MoePlan(T, k, n_experts, offsets, order, slots)
+    at = buf.data_ptr()
+    _call(lib().pql_moe_plan, "moe_plan", device, ids.data_ptr(), T, k, n_experts, at + 8 * P, at, at + 4 * P, ws, wsn)
     return plan
 
 
@@ -675,15 +690,15 @@ def moe_qgemm(a: QTensor, w: QTensor, plan: MoePlan, gather: bool = False,
     P, N = plan.tokens * plan.top_k, w.rows // plan.n_experts
     if a.rows != (plan.tokens if gather else P):
         raise ValueError(f"expected an activation of {plan.tokens if gather else P} rows, got {a.rows}")
+    device = w.device
     if out is None:
-        out = torch.empty((P, N), dtype=torch.bfloat16, device=w.device)
-    _check_out(out, P, N, w.device)
-    _on_device(w.device)
-    with _device_of(w.device):
-        _check(lib().pql_moe_qgemm(_scheme(w.scheme), a.codes.data_ptr(), a.scales.data_ptr(), a.rows, int(gather),
-                                   w.codes.data_ptr(), w.scales.data_ptr(), plan.offsets.data_ptr(),
-                                   plan.order.data_ptr(), plan.tokens, plan.top_k, plan.n_experts, N, w.cols,
-                                   out.data_ptr(), out.stride(0) if P > 1 else N, _stream(w.device)), "moe_qgemm")
+        out, ldc = torch.empty((P, N), dtype=torch.bfloat16, device=device), N
+    else:
+        ldc = _check_rows(out, "out", P, N, device)
+    _on_device(device)
+    _call(lib().pql_moe_qgemm, "moe_qgemm", device, SCHEMES[w.scheme], a.codes.data_ptr(), a.scales.data_ptr(), a.rows,
+          gather, w.codes.data_ptr(), w.scales.data_ptr(), plan.offsets.data_ptr(), plan.order.data_ptr(), plan.tokens,
+          plan.top_k, plan.n_experts, N, w.cols, out.data_ptr(), ldc)
     return out
 
 
@@ -713,11 +728,9 @@ def swiglu_quantize(x: torch.Tensor, scheme: str, plan: MoePlan | None = None, o
         q = out
     else:
         q = _alloc_q(scheme, "activation", rows, cols, x.device)
-    with _device_of(x.device):
-        _check(lib().pql_swiglu_quantize(_scheme(scheme), x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else 2 * cols,
-                                         None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_experts,
-                                         q.codes.data_ptr(), q.scales.data_ptr(), _stream(x.device)),
-               "swiglu_quantize")
+    _call(lib().pql_swiglu_quantize, "swiglu_quantize", x.device, SCHEMES[scheme], x.data_ptr(), rows, cols,
+          x.stride(0) if rows > 1 else 2 * cols, None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_experts,
+          q.codes.data_ptr(), q.scales.data_ptr())
     return q
 
 
@@ -730,22 +743,16 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor, add: torc
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         raise ValueError("y must be a 2-D tensor")
     N = y.shape[1]
-    _check_out(y, P, N, device, "y")
+    ldy = _check_rows(y, "y", P, N, device)
     _check_vector(weights, "weights", torch.float32, P, device)
-    if add is not None:
-        _check_out(add, T, N, device, "add")
+    ldadd = N if add is None else _check_rows(add, "add", T, N, device)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=device)
-    _check_out(out, T, N, device)
+        out, ldo = torch.empty((T, N), dtype=torch.bfloat16, device=device), N
+    else:
+        ldo = _check_rows(out, "out", T, N, device)
     _on_device(device)
-
-    def ld(t):
-        return t.stride(0) if t.shape[0] > 1 else N
-
-    with _device_of(device):
-        _check(lib().pql_moe_combine(y.data_ptr(), P, ld(y), plan.slots.data_ptr(), weights.data_ptr(), T, plan.top_k,
-                                     N, _ptr(add), N if add is None else ld(add), out.data_ptr(), ld(out),
-                                     _stream(device)), "moe_combine")
+    _call(lib().pql_moe_combine, "moe_combine", device, y.data_ptr(), P, ldy, plan.slots.data_ptr(), weights.data_ptr(),
+          T, plan.top_k, N, _ptr(add), ldadd, out.data_ptr(), ldo)
     return out
 
 

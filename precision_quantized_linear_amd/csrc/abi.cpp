@@ -914,7 +914,7 @@ pql_status pql_moe_plan(const int32_t* ids, int64_t T, int64_t k, int64_t E, int
   const pql_status st = moe_plan_impl(ids, T, k, E, offsets, order, slots, workspace, workspace_bytes, stream);
   if (log_enabled())
     log_moe(st, "moe_plan", shape_text("T=%lld k=%lld E=%lld", (long long)T, (long long)k, (long long)E), false,
-            st == PQL_OK ? pql::moe_plan_kernel_name(T * k, (int)E) : "", stream);
+            st == PQL_OK ? pql::moe_plan_kernel_name(T * k) : "", stream);
   return st;
 }
 

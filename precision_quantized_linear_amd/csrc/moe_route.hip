@@ -218,80 +218,136 @@ hipError_t launch_route_type(const RouteArgs& r, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------- grouping
-// A stable counting sort by expert.  One workgroup walks the assignments in rounds of 512:
-// a wave ranks its 64 ids among themselves with one ballot per bit of the id, the waves'
-// counts per expert are summed in wave order, and every round starts where the last ended.
+// A stable counting sort by expert.  A workgroup owns a contiguous chunk of the assignments and
+// a wave a contiguous part of the chunk, walked 64 ids at a time: a wave ranks its 64 ids among
+// themselves with one ballot per bit of the id, and adds what it has counted before (a counter
+// per wave and expert in LDS that only this wave touches, so no atomics and no order to lose).
+// Up to kPlanChunk assignments take one launch of one workgroup; more take two: k_moe_count
+// writes each chunk's counts, and every workgroup of k_moe_place sums those of all chunks and
+// of the chunks before its own.
 constexpr int kPlanThreads = 512, kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanChunk = 2048;
+constexpr int kPlanMaxBlocks = 256;   // beyond 2^19 assignments the chunks grow instead
 
-__global__ __launch_bounds__(kPlanThreads) void k_moe_plan(const int32_t* __restrict__ ids, int P, int E,
-                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ order,
-                                                           int32_t* __restrict__ slots) {
-  extern __shared__ int plan_lds[];
-  int* next = plan_lds;              // [E]: where an expert's next assignment goes
-  int* count = plan_lds + E;         // [kPlanWaves][E]
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int bits = 32 - __builtin_clz(E);   // ids 0 .. E (E: not held here)
-  for (int e = t; e < E; e += kPlanThreads) next[e] = 0;
+int64_t plan_chunk(int64_t P) {
+  const int64_t per = (P + kPlanMaxBlocks - 1) / kPlanMaxBlocks;
+  return std::max<int64_t>(kPlanChunk, (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads);
+}
+int plan_blocks(int64_t P) { return (int)std::max<int64_t>(1, (P + plan_chunk(P) - 1) / plan_chunk(P)); }
+
+__global__ __launch_bounds__(kPlanThreads) void k_moe_count(const int32_t* __restrict__ ids, int P, int E, int chunk,
+                                                            int32_t* __restrict__ counts) {
+  __shared__ int n[kMoeMaxExperts];
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) n[e] = 0;
   __syncthreads();
-  for (int i = t; i < P; i += kPlanThreads) {
+  const int end = (int)std::min<int64_t>(P, (int64_t)(blockIdx.x + 1) * chunk);
+  for (int i = blockIdx.x * chunk + threadIdx.x; i < end; i += kPlanThreads) {
     const int id = ids[i];
-    if ((unsigned)id < (unsigned)E) atomicAdd(&next[id], 1);   // integer counts: any order gives the same
+    if ((unsigned)id < (unsigned)E) atomicAdd(&n[id], 1);   // whole numbers: any order gives the same
   }
   __syncthreads();
-  if (wave == 0) {   // exclusive prefix over the experts
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int n = e0 + lane < E ? next[e0 + lane] : 0;
-      int s = n;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(s, o);
-        if (lane >= o) s += u;
-      }
-      if (e0 + lane < E) {
-        next[e0 + lane] = carry + s - n;
-        offsets[e0 + lane] = carry + s - n;
-      }
-      carry += __shfl(s, 63);
-    }
-    if (lane == 0) offsets[E] = carry;
-    if (lane == 0) count[0] = carry;
-  }
-  __syncthreads();
-  const int total = count[0];
-  __syncthreads();
-  for (int i = total + t; i < P; i += kPlanThreads) order[i] = -1;
-  for (int base = 0; base < P; base += kPlanThreads) {
-    const int i = base + t;
-    int id = i < P ? ids[i] : E;
-    if ((unsigned)id >= (unsigned)E) id = E;
-    for (int q = t; q < kPlanWaves * E; q += kPlanThreads) count[q] = 0;
-    __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[(int64_t)blockIdx.x * E + e] = n[e];
+}
+
+// counts: [gridDim.x][E] from k_moe_count; unused by a single workgroup.
+__global__ __launch_bounds__(kPlanThreads) void k_moe_place(const int32_t* __restrict__ ids, int P, int E, int chunk,
+                                                            const int32_t* __restrict__ counts,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                                                            int32_t* __restrict__ slots) {
+  __shared__ int seen[kPlanWaves][kMoeMaxExperts];   // per wave: assignments of an expert so far
+  __shared__ int start[kMoeMaxExperts];
+  __shared__ int part[kMoeMaxExperts / 64 + 1];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int bits = 32 - __builtin_clz(E);            // ids 0 .. E (E: takes no part)
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  const int share = chunk / kPlanWaves;              // a multiple of 64
+  const int begin = (int)std::min<int64_t>(P, (int64_t)blockIdx.x * chunk + (int64_t)wave * share);
+  const int end = std::min(P, begin + share);
+  for (int e = lane; e < E; e += 64) seen[wave][e] = 0;
+  auto id_at = [&](int i) __attribute__((always_inline)) {
+    const int id = i < end ? ids[i] : E;
+    return (unsigned)id < (unsigned)E ? id : E;
+  };
+  auto lanes_with = [&](int id) __attribute__((always_inline)) {
     uint64_t same = ~uint64_t(0);
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot((id >> b) & 1);
       same &= (id >> b) & 1 ? set : ~set;
     }
-    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-    if (id < E && rank == 0) count[wave * E + id] = __popcll(same);
-    __syncthreads();
-    for (int e = t; e < E; e += kPlanThreads) {
-      int at = next[e];
-      for (int w = 0; w < kPlanWaves; ++w) {
-        const int n = count[w * E + e];
-        count[w * E + e] = at;
-        at += n;
-      }
-      next[e] = at;
-    }
-    __syncthreads();
-    if (i < P) {
-      const int place = id < E ? count[wave * E + id] + rank : -1;
-      slots[i] = place;
-      if (place >= 0) order[place] = i;
-    }
-    __syncthreads();
+    return same;
+  };
+  // Only this wave touches seen[wave], and LDS runs a wave's accesses in order; the fences
+  // keep the compiler from reordering or merging them across lanes.
+  for (int i0 = begin; i0 < end; i0 += 64) {
+    const int id = id_at(i0 + lane);
+    const uint64_t same = lanes_with(id);
+    if (id < E && !(same & below)) seen[wave][id] += __popcll(same);
+    asm volatile("" ::: "memory");
   }
+  __syncthreads();
+
+  // per expert: all of its assignments, those of earlier chunks, and the waves' starts
+  for (int e = t; e < E; e += kPlanThreads) {
+    int all = 0, before = 0;
+    if (gridDim.x == 1) {
+#pragma unroll
+      for (int w = 0; w < kPlanWaves; ++w) all += seen[w][e];
+    } else {
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int n = counts[(int64_t)b * E + e];
+        all += n;
+        before += b < (int)blockIdx.x ? n : 0;
+      }
+    }
+    start[e] = all;
+    int at = before;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int n = seen[w][e];
+      seen[w][e] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  // exclusive prefix of start[] over the experts: 64 at a time, then the sums before them
+  for (int e0 = wave * 64; e0 < E; e0 += kPlanThreads) {
+    const int n = e0 + lane < E ? start[e0 + lane] : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(s, o);
+      if (lane >= o) s += u;
+    }
+    if (e0 + lane < E) start[e0 + lane] = s - n;
+    if (lane == 63) part[e0 / 64] = s;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int q = 0; q < (E + 63) / 64; ++q) total += part[q];
+  for (int e = t; e < E; e += kPlanThreads) {
+    int base = start[e];
+    for (int q = 0; q < e / 64; ++q) base += part[q];
+    start[e] = base;
+    if (blockIdx.x == 0) offsets[e] = base;
+  }
+  if (blockIdx.x == 0 && t == 0) offsets[E] = total;
+  __syncthreads();
+
+  for (int i0 = begin; i0 < end; i0 += 64) {
+    const int i = i0 + lane;
+    const int id = id_at(i);
+    const uint64_t same = lanes_with(id);
+    int place = -1;
+    if (id < E) place = start[id] + seen[wave][id] + __popcll(same & below);
+    asm volatile("" ::: "memory");
+    if (id < E && !(same & below)) seen[wave][id] += __popcll(same);
+    asm volatile("" ::: "memory");
+    if (i < end) slots[i] = place;
+    if (place >= 0) order[place] = i;
+  }
+  for (int64_t i = total + (int64_t)blockIdx.x * kPlanThreads + t; i < P; i += (int64_t)gridDim.x * kPlanThreads)
+    order[i] = -1;
 }
 
 }  // namespace
@@ -304,13 +360,19 @@ hipError_t launch_moe_route(int dtype, const RouteArgs& r, hipStream_t st) {
   }
 }
 
-size_t moe_plan_ws_bytes(int64_t, int) { return 0; }
-const char* moe_plan_kernel_name(int64_t, int) { return "k_moe_plan"; }
+size_t moe_plan_ws_bytes(int64_t P, int E) {
+  const int blocks = plan_blocks(P);
+  return blocks > 1 ? sizeof(int32_t) * (size_t)blocks * (size_t)E : 0;
+}
+
+const char* moe_plan_kernel_name(int64_t P) { return plan_blocks(P) > 1 ? "k_moe_count+k_moe_place" : "k_moe_place"; }
 
 hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* slots,
-                           int32_t*, hipStream_t st) {
-  const size_t lds = sizeof(int) * (size_t)E * (kPlanWaves + 1);   // 36,864 bytes at most (E = 1024)
-  hipLaunchKernelGGL(k_moe_plan, dim3(1), dim3(kPlanThreads), lds, st, ids, (int)P, E, offsets, order, slots);
+                           int32_t* ws, hipStream_t st) {
+  const int blocks = plan_blocks(P), chunk = (int)plan_chunk(P);
+  if (blocks > 1) hipLaunchKernelGGL(k_moe_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws);
+  hipLaunchKernelGGL(k_moe_place, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws, offsets, order,
+                     slots);
   return hipGetLastError();
 }
 

@@ -153,7 +153,7 @@ constexpr int64_t kMoeMaxRows = (int64_t(1) << 24) - 1;
 hipError_t launch_moe_route(int dtype, const RouteArgs& r, hipStream_t st);
 // Workspace of the grouping (0: none) and its launch; ws holds that many bytes.
 size_t moe_plan_ws_bytes(int64_t P, int E);
-const char* moe_plan_kernel_name(int64_t P, int E);
+const char* moe_plan_kernel_name(int64_t P);
 hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* slots,
                            int32_t* ws, hipStream_t st);
 

@@ -859,6 +859,7 @@ static pql_status moe_route_impl(int score, int dtype, const void* logits, int64
   r.score = score;
   r.bias = bias;
   r.groups = (int)groups;
+  r.per_group = (int)(E / groups);
   r.top_groups = (int)top_groups;
   r.group_score = group_score;
   r.renormalize = renormalize != 0;

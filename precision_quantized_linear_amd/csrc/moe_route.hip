@@ -7,8 +7,13 @@
 //   score is its best choice, or the sum of its two best);  ties go to the lowest index;
 //   weight = s (without the bias), divided by the sum over the k where asked, times a factor.
 // With a bias two experts' choices can be closer than fp32 resolves them, and then the order
-// itself would depend on rounding, so scores and choices are formed in fp64 there; without
-// one the keys are the logits, compared exactly.
+// itself would depend on rounding, so the order is that of the fp64 choices.  Forming E of them
+// per token in fp64 costs more than everything else, so the choices are formed in fp32 with a
+// bound on their error (delta), the k best and whatever lies within 2 delta of the k-th become
+// candidates, one per lane, and only those are evaluated in fp64 and ranked.  Where the fp32
+// choices cannot settle it (more candidates than lanes, group scores within the bound of each
+// other) the wave takes the fp64 path for all E.  Without a bias the keys are the logits,
+// compared exactly.
 #include <algorithm>
 #include <type_traits>
 
@@ -20,6 +25,9 @@ namespace pql {
 namespace {
 
 constexpr int kRouteThreads = 256;
+// Up to this many tokens a wave takes one token (E = 256 with bias and groups: 2048 tokens 8.2 us
+// a launch against 10.4 with four tokens a wave, 8192 tokens 19.3 against 13.7).
+constexpr int64_t kRouteWide = 2048;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr double kNegInfD = -__builtin_huge_val();
 
@@ -30,173 +38,446 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   else return (float)static_cast<const _Float16*>(p)[i];
 }
 
+// Reductions over a token's L lanes, the result in every lane: DPP inside rows of 16, lane
+// swaps between rows (no LDS permutes: k rounds of two reductions each are one long chain).
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp_of(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const v2i w = __builtin_bit_cast(v2i, v);
+    return __builtin_bit_cast(T, v2i{dpp<CTRL>(w.x), dpp<CTRL>(w.y)});
+  } else {
+    return __builtin_bit_cast(T, dpp<CTRL>(__builtin_bit_cast(int, v)));
+  }
+}
+template <int L, class F, class T>
+__device__ __forceinline__ T reduce(T v, F f) {
+  static_assert(L == 16 || L == 32 || L == 64);
+  auto step = [&](auto ctrl) __attribute__((always_inline)) {
+    v = f(v, dpp_of<decltype(ctrl)::value>(v));
+  };
+  step(std::integral_constant<int, 0xB1>{});    // lane ^ 1
+  step(std::integral_constant<int, 0x4E>{});    // lane ^ 2
+  step(std::integral_constant<int, 0x141>{});   // the other quad of 8
+  step(std::integral_constant<int, 0x140>{});   // the other 8 of 16
+  auto swap = [&](auto rows) __attribute__((always_inline)) {   // both sides' values, in every lane
+    constexpr int n = sizeof(T) / 4;
+    uint32_t w[2], a[2], b[2];
+    __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if constexpr (decltype(rows)::value == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(w[i], w[i], false, false);
+        a[i] = p[0];
+        b[i] = p[1];
+      } else {
+        const auto p = __builtin_amdgcn_permlane32_swap(w[i], w[i], false, false);
+        a[i] = p[0];
+        b[i] = p[1];
+      }
+    }
+    T va, vb;
+    __builtin_memcpy(&va, a, sizeof(T));
+    __builtin_memcpy(&vb, b, sizeof(T));
+    v = f(va, vb);
+  };
+  if constexpr (L >= 32) swap(std::integral_constant<int, 16>{});
+  if constexpr (L >= 64) swap(std::integral_constant<int, 32>{});
+  return v;
+}
+template <int L> __device__ __forceinline__ float lanes_max(float v) { return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); }); }
+template <int L> __device__ __forceinline__ int lanes_min(int v) { return reduce<L>(v, [](int a, int b) { return std::min(a, b); }); }
+template <int L> __device__ __forceinline__ float lanes_sum(float v) { return reduce<L>(v, [](float a, float b) { return a + b; }); }
+template <int L> __device__ __forceinline__ double lanes_max(double v) { return reduce<L>(v, [](double a, double b) { return fmax(a, b); }); }
+template <int L> __device__ __forceinline__ double lanes_sum(double v) { return reduce<L>(v, [](double a, double b) { return a + b; }); }
+
+// 1 / (1 + exp(-x)) and exp(x - top): fp64 for the order and for weights too small for fp32.
+__device__ __forceinline__ double score64(bool softmax, float x, double top, double denom) {
+  if (!(x > kNegInf)) return 0.0;
+  return softmax ? exp((double)x - top) / denom : 1.0 / (1.0 + exp(-(double)x));
+}
+
+// The best key of a lane and its place among the lane's V.
+template <int V, class Key>
+__device__ __forceinline__ void lane_best(const Key (&key)[V], Key out, Key& best, int& at) {
+  best = out;
+  at = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (key[v] > best) {
+      best = key[v];
+      at = v;
+    }
+}
+
+// One round: the best key over the token's lanes, taken out of its lane; its expert (the lowest
+// among equals) or -1.
+template <int L, int V, class Key>
+__device__ __forceinline__ int take_best(Key (&key)[V], Key out, Key& best, int& at, int lane, Key& value) {
+  value = lanes_max<L>(best);
+  const bool found = value > out;
+  const int id = lanes_min<L>(found && best == value ? at * L + lane : 0x7fffffff);
+  if (id == at * L + lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v == at) key[v] = out;
+    lane_best<V>(key, out, best, at);
+  }
+  return found ? id : -1;
+}
+
+// i / n for 0 <= i < 1024, 1 <= n <= 1024: (i + 1/2) / n is at least 1 / (2 n) away from a whole
+// number, far more than the fp32 error, so rounding down is exact (an integer division is ~30
+// instructions, and a lane needs one per logit).
+__device__ __forceinline__ int small_div(int i, float inverse_n) { return (int)(((float)i + 0.5f) * inverse_n); }
+
+// Groups of experts: the mask of the kept ones.  `choice` (LDS, the token's own) holds the
+// choices by expert, `score` room for the groups'.  Scores within `slack` of each other are not told apart: then
+// `unsure` is set (slack 0: equal scores go to the lowest group).
+template <int L, class Key>
+__device__ __forceinline__ uint64_t kept_groups(const RouteArgs& r, int per, const Key* choice, Key* score, int lane,
+                                                Key slack, bool& unsure) {
+  const float inverse_per = 1.0f / (float)per;
+  const Key out = (Key)kNegInfD;
+  // share lanes (1, 2, 4 or 8) read a group together
+  const int share = r.groups * 8 <= L ? 8 : r.groups * 4 <= L ? 4 : r.groups * 2 <= L ? 2 : 1;
+  for (int g0 = 0; g0 < r.groups; g0 += L) {
+    const int g = g0 + lane / share, part = lane & (share - 1);
+    Key a = out, b = out;   // the two best
+    if (g < r.groups) {
+      int at = (threadIdx.x & 63) - part;   // groups start apart: they and the tokens would share LDS banks
+      if (at >= per) at -= small_div(at, inverse_per) * per;
+#pragma unroll 4
+      for (int i = part; i < per; i += share) {
+        const int place = at + i >= per ? at + i - per : at + i;
+        const Key c = choice[g * per + place];
+        b = c > a ? a : (c > b ? c : b);
+        a = c > a ? c : a;
+      }
+    }
+    auto merge = [&](auto ctrl) __attribute__((always_inline)) {
+      const Key oa = dpp_of<decltype(ctrl)::value>(a), ob = dpp_of<decltype(ctrl)::value>(b);
+      const Key low = oa < a ? oa : a, high = ob > b ? ob : b;
+      a = oa > a ? oa : a;
+      b = low > high ? low : high;
+    };
+    if (share > 1) merge(std::integral_constant<int, 0xB1>{});
+    if (share > 2) merge(std::integral_constant<int, 0x4E>{});
+    if (share > 4) merge(std::integral_constant<int, 0x141>{});
+    if (g < r.groups && part == 0) score[g] = r.group_score == 1 && b > out ? a + b : a;
+  }
+  asm volatile("" ::: "memory");   // a token's lanes share a wave, whose LDS accesses run in order
+  uint64_t kept = 0;
+  bool open = false;
+  for (int g0 = 0; g0 < r.groups; g0 += L) {
+    const int g = std::min(g0 + lane, r.groups - 1);
+    const Key s = score[g];
+    int above = 0, near = 0;   // certainly above; above or too close to tell
+#pragma unroll 4
+    for (int h = 0; h < r.groups; ++h) {
+      const Key q = score[h];
+      above += q > s + slack || (slack == 0 && q == s && h < g);
+      near += h != g && q > s - slack;
+    }
+    const bool mine = above < r.top_groups && g0 + lane < r.groups;
+    open |= slack > 0 && mine && near >= r.top_groups;
+    const uint64_t bits = __ballot(mine) >> (threadIdx.x & 63 & ~(L - 1));
+    kept |= (L == 64 ? bits : bits & ((uint64_t(1) << (L & 63)) - 1)) << g0;
+  }
+  const uint64_t any = __ballot(open) >> (threadIdx.x & 63 & ~(L - 1));
+  unsure |= (L == 64 ? any : any & ((uint64_t(1) << (L & 63)) - 1)) != 0;
+  return kept;
+}
+
 // L lanes per token, V logits per lane: lane i of the token's L holds experts i, i + L, ...
-template <int DT, int L, int V, bool WIDE>
+template <int DT, int L, int V, bool BIASED>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route(RouteArgs r) {
-  using Key = std::conditional_t<WIDE, double, float>;
-  constexpr Key kOut = WIDE ? (Key)kNegInfD : (Key)kNegInf;
   constexpr int kTokens = kRouteThreads / L;
-  __shared__ double choice_lds[kTokens][L * V];   // groups only: the choices by expert
-  __shared__ double group_lds[kTokens][64];
+  __shared__ double choice_lds[kTokens][L * V + 8];   // groups only: the choices by expert (padded: tokens on other banks)
+  __shared__ double group_lds[kTokens][kMoeMaxGroups];
   const int lane = threadIdx.x % L, sub = threadIdx.x / L;
   const int64_t token = (int64_t)blockIdx.x * kTokens + sub;
   const int64_t t = std::min<int64_t>(token, r.T - 1);   // lanes past the last token repeat it, and store nothing
   const int E = r.E;
+  const bool softmax = r.score == 0;
+  const int per = r.per_group;
+  const float inverse_per = 1.0f / (float)per;
 
-  float x[V];
-  bool broken = false;
+  float x[V], bias[V];
+  bool bad = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = v * L + lane;
     x[v] = e < E ? load_logit<DT>(r.logits, t * r.ldl + e) : kNegInf;
-    broken |= !(x[v] < -kNegInf);   // NaN or +inf
+    if constexpr (BIASED) bias[v] = e < E ? r.bias[e] : kNegInf;
   }
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) broken |= (bool)__shfl_xor((int)broken, o, L);
   float top = kNegInf;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (broken) x[v] = kNegInf;
+    bad |= !(x[v] < -kNegInf);   // NaN or +inf
     top = fmaxf(top, x[v]);
   }
+  const bool broken = lanes_min<L>(bad ? 0 : 1) == 0;
+  if (broken) {
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, L));
-  const double dtop = top > kNegInf ? (double)top : 0.0;
-  const bool softmax = r.score == 0;
-
-  // the softmax's denominator (every expert takes part, masked ones with 0)
-  double denom = 1.0;
-  if (softmax) {
-    double sum = 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum += x[v] > kNegInf ? exp((double)x[v] - dtop) : 0.0;
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor(sum, o, L);
-    denom = sum;
+    for (int v = 0; v < V; ++v) x[v] = kNegInf;
+    top = kNegInf;
   }
-  auto score = [&](float xv) -> double {
-    if (!(xv > kNegInf)) return 0.0;
-    return softmax ? exp((double)xv - dtop) / denom : 1.0 / (1.0 + exp(-(double)xv));
+  top = lanes_max<L>(top);
+  if (!(top > kNegInf)) top = 0.0f;
+  auto score32 = [&](float xv, float denom) __attribute__((always_inline)) {   // 0 for an unavailable expert
+    return softmax ? expf(xv - top) / denom : 1.0f / (1.0f + expf(-xv));
+  };
+  auto rough = [&](float xv, float inverse) __attribute__((always_inline)) {   // the same within the bound below
+    constexpr float kLog2e = 1.44269504f;
+    return softmax ? __builtin_amdgcn_exp2f((xv - top) * kLog2e) * inverse
+                   : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(xv * -kLog2e));
+  };
+  float denom = 1.0f;   // the softmax's (unavailable experts add 0)
+  if (softmax && (BIASED || !r.renormalize || r.groups > 1)) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum += __builtin_amdgcn_exp2f((x[v] - top) * 1.44269504f);
+    denom = lanes_sum<L>(sum);
+  }
+  const float inverse = BIASED || r.groups > 1 ? __builtin_amdgcn_rcpf(denom) : 1.0f;
+  auto denom64 = [&]() __attribute__((always_inline)) {   // rare: reads the logits again
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += L) {
+      const float xv = load_logit<DT>(r.logits, t * r.ldl + e);
+      sum += !broken && xv > kNegInf ? exp((double)xv - (double)top) : 0.0;
+    }
+    return lanes_sum<L>(sum);
   };
 
-  Key key[V];
+  // ---- fp32 keys, and the bound of their error, in units of u = 2^-24 (half an ulp of 1).  In
+  // rough() the exponential of an argument y is off by (1.5 |y| + 2) u relative: y log2 e is
+  // rounded, as is log2 e, and the instruction is within one ulp.
+  //   sigmoid: that enters as s (1 - s) (1.5 |y| + 2) <= 0.9, the sum and the reciprocal of a
+  //   value below 1 add 3: below 4 u.
+  //   softmax: it enters as s (1.5 |y| + 2) <= 2.6; the denominator's relative error, the terms'
+  //   (their mean |y| is below ln E = 7) and at most 22 roundings, is below 35, its reciprocal
+  //   and the product add 3: below 41 u.
+  // Adding the bias rounds once more; 6 and 48, and 2 |c| u, leave room.
+  float key[V];
+  float biggest = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * L + lane;
-    key[v] = kOut;
+    key[v] = kNegInf;
     if (x[v] > kNegInf) {
-      if constexpr (WIDE) {
-        const double c = score(x[v]) + (double)r.bias[e];
-        if (c > kNegInfD) key[v] = c;
+      if constexpr (BIASED) {
+        const float c = rough(x[v], inverse) + bias[v];
+        if (c > kNegInf) {
+          key[v] = c;
+          biggest = fmaxf(biggest, fabsf(c));
+        }
       } else {
         key[v] = x[v];
       }
     }
   }
-
+  bool unsure = false;
+  float delta = 0.0f;
+  if constexpr (BIASED) {
+    delta = ((softmax ? 48.0f : 6.0f) + 2.0f * lanes_max<L>(biggest)) * 0x1p-24f;
+    unsure = !(delta < 1.0f) || r.k > L - 2;   // huge biases; no lane left for a further candidate
+  }
   if (r.groups > 1) {
-    const int per = E / r.groups;
-    const bool top2 = r.group_score == 1;
+    const bool exact = !BIASED && r.group_score == 0;   // the logits themselves
+    float* choice = reinterpret_cast<float*>(choice_lds[sub]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * L + lane;
-      double c = kNegInfD;
-      if (key[v] > kOut) {
-        if constexpr (WIDE) c = key[v];
-        else c = top2 ? score(x[v]) : (double)x[v];
+      float c = key[v];
+      if constexpr (!BIASED) {
+        if (r.group_score == 1 && c > kNegInf) c = rough(c, inverse);
       }
-      if (e < E) choice_lds[sub][e] = c;
+      choice[v * L + lane] = c;
     }
-    __syncthreads();
-    for (int g = lane; g < r.groups; g += L) {
-      double a = kNegInfD, b = kNegInfD;   // the two best
-      for (int i = 0; i < per; ++i) {
-        const double c = choice_lds[sub][g * per + i];
-        b = fmax(b, fmin(a, c));
-        a = fmax(a, c);
+    asm volatile("" ::: "memory");
+    const float slack = exact ? 0.0f : 4.0f * (BIASED ? delta : 50.0f * 0x1p-24f);
+    bool level = false;   // group scores too close for fp32
+    uint64_t kept = kept_groups<L, float>(r, per, choice, reinterpret_cast<float*>(group_lds[sub]), lane, slack, level);
+    if (__ballot(level)) {   // their choices in fp64, one token at a time on all 64 lanes
+      asm volatile("" ::: "memory");
+      const int wl = threadIdx.x & 63;
+#pragma unroll 1
+      for (int q = 0; q < 64 / L; ++q) {
+        if (!__shfl((int)level, q * L)) continue;
+        const int row = sub - wl / L + q;   // the token's place in the workgroup
+        const int64_t tq = std::min<int64_t>((int64_t)blockIdx.x * kTokens + row, r.T - 1);
+        const double tops = (double)__shfl(top, q * L);
+        double z = 0.0;
+#pragma unroll 1
+        for (int e = wl; softmax && e < E; e += 64) z += score64(true, load_logit<DT>(r.logits, tq * r.ldl + e), tops, 1.0);
+        z = softmax ? lanes_sum<64>(z) : 1.0;
+#pragma unroll 1
+        for (int e = wl; e < E; e += 64) {
+          const float xv = load_logit<DT>(r.logits, tq * r.ldl + e);
+          double c = kNegInfD;
+          if (xv > kNegInf) {
+            c = score64(softmax, xv, tops, z);
+            if constexpr (BIASED) c = c + (double)r.bias[e] > kNegInfD ? c + (double)r.bias[e] : kNegInfD;
+          }
+          choice_lds[row][e] = c;
+        }
       }
-      group_lds[sub][g] = top2 && b > kNegInfD ? a + b : a;
-    }
-    __syncthreads();
-    uint64_t kept = 0;
-    for (int g = 0; g < r.groups; ++g) {
-      const double s = group_lds[sub][g];
-      int rank = 0;
-      for (int h = lane; h < r.groups; h += L) {
-        const double q = group_lds[sub][h];
-        rank += q > s || (q == s && h < g);
-      }
-#pragma unroll
-      for (int o = 1; o < L; o <<= 1) rank += __shfl_xor(rank, o, L);
-      if (rank < r.top_groups) kept |= uint64_t(1) << g;
+      asm volatile("" ::: "memory");
+      bool never = false;
+      const uint64_t kept64 = kept_groups<L, double>(r, per, choice_lds[sub], group_lds[sub], lane, 0.0, never);
+      if (level) kept = kept64;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (!((kept >> std::min((v * L + lane) / per, 63)) & 1)) key[v] = kOut;
+      if (!((kept >> std::min(small_div(v * L + lane, inverse_per), 63)) & 1)) key[v] = kNegInf;
   }
 
-  // k rounds: the best key of the token's lanes, lowest index first among equals
-  constexpr int kSlots = L >= 32 ? 1 : 32 / L;   // results a lane keeps (k <= 32)
+  // ---- k rounds.  Lane j % L keeps the j-th (k <= 32).
+  constexpr int kSlots = L >= 32 ? 1 : 32 / L;
   int my_id[kSlots];
-  float my_x[kSlots];
+  double my_w[kSlots];   // scores, then weights
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
     my_id[q] = -1;
-    my_x[q] = kNegInf;
+    my_w[q] = 0.0;
   }
-  for (int j = 0; j < r.k; ++j) {
-    Key best = kOut;
-    int at = 0x7fffffff;
-    float bx = kNegInf;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] > best) {
-        best = key[v];
-        at = v * L + lane;
-        bx = x[v];
+  int rank0 = lane;      // the slot that lane's first result goes to
+  if (!__ballot(unsure)) {
+    float best, value = 0.0f, last = -kNegInf;
+    int at;
+    lane_best<V>(key, kNegInf, best, at);
+    bool close = false;   // two neighbours in the order within the error bound of each other
+    int j = 0;
+    for (; j < r.k; ++j) {
+      const int id = take_best<L, V>(key, kNegInf, best, at, lane, value);
+      if constexpr (BIASED) {
+        close |= value > kNegInf && last - value <= 2.0f * delta;
+        last = value;
       }
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-      const Key ob = __shfl_xor(best, o, L);
-      const int oa = __shfl_xor(at, o, L);
-      const float ox = __shfl_xor(bx, o, L);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-        bx = ox;
+      for (int q = 0; q < kSlots; ++q)
+        if (j == q * L + lane) my_id[q] = id;
+    }
+    if constexpr (BIASED) {
+      // whatever lies within 2 delta of the k-th may belong before it
+      const float least = value - 2.0f * delta;
+      bool more = value > kNegInf && lanes_max<L>(best) >= least;
+      close |= more;
+      for (; j < L && __ballot(more); ++j) {
+        const int id = take_best<L, V>(key, kNegInf, best, at, lane, value);
+        if (j == lane) my_id[0] = id;
+        more = more && value > kNegInf && lanes_max<L>(best) >= least;
+      }
+      unsure = more;   // more candidates than lanes
+    }
+    if (__ballot(close)) {   // rank the candidates by their fp64 choices
+      const double z = softmax ? denom64() : 1.0;
+      const int id = my_id[0];
+      const float xi = id >= 0 ? load_logit<DT>(r.logits, t * r.ldl + id) : kNegInf;
+      my_w[0] = score64(softmax, xi, (double)top, z);
+      const double c = id >= 0 ? my_w[0] + (double)r.bias[id] : kNegInfD;
+      rank0 = 0;
+      for (int q = 0; q < j; ++q) {
+        const double oc = __shfl(c, q, L);
+        const int oid = __shfl(id, q, L);
+        rank0 += oid >= 0 && (id < 0 || oc > c || (oc == c && oid < id));
+      }
+      if (id < 0) rank0 = std::max(rank0, lane);   // empty slots after all candidates
+    } else {
+      bool tiny = false;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (my_id[q] >= 0) {
+          const float xi = load_logit<DT>(r.logits, t * r.ldl + my_id[q]);
+          const float s = score32(xi, !BIASED && r.renormalize ? 1.0f : denom);
+          my_w[q] = (double)s;
+          tiny |= s < 0x1p-100f;
+        }
+      if (__ballot(tiny)) {   // weights near or below the end of fp32's range: in fp64
+        const double z = softmax ? denom64() : 1.0;
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (my_id[q] >= 0)
+            my_w[q] = score64(softmax, load_logit<DT>(r.logits, t * r.ldl + my_id[q]), (double)top, z);
       }
     }
-    const bool found = best > kOut;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (found && at == v * L + lane) key[v] = kOut;
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q)
-      if (found && j == q * L + lane) {
-        my_id[q] = at;
-        my_x[q] = bx;
-      }
   }
 
-  double w[kSlots], sum = 0.0;
+  // ---- all of it in fp64, where fp32 did not settle the order (wave-uniform)
+  if (__ballot(unsure)) {
+    const double z = softmax ? denom64() : 1.0;
+    double wide[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      wide[v] = kNegInfD;
+      if (x[v] > kNegInf) {
+        if constexpr (BIASED) {
+          const double c = score64(softmax, x[v], (double)top, z) + (double)r.bias[v * L + lane];
+          if (c > kNegInfD) wide[v] = c;
+        } else {
+          wide[v] = (double)x[v];
+        }
+      }
+    }
+    if (r.groups > 1) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        double c = wide[v];
+        if constexpr (!BIASED) {
+          if (r.group_score == 1 && c > kNegInfD) c = score64(softmax, x[v], (double)top, z);
+        }
+        choice_lds[sub][v * L + lane] = c;
+      }
+      asm volatile("" ::: "memory");
+      bool never = false;
+      const uint64_t kept = kept_groups<L, double>(r, per, choice_lds[sub], group_lds[sub], lane, 0.0, never);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (!((kept >> std::min(small_div(v * L + lane, inverse_per), 63)) & 1)) wide[v] = kNegInfD;
+    }
+    double best, value;
+    int at;
+    lane_best<V>(wide, kNegInfD, best, at);
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) my_id[q] = -1;
+    for (int j = 0; j < r.k; ++j) {
+      const int id = take_best<L, V>(wide, kNegInfD, best, at, lane, value);
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (j == q * L + lane) my_id[q] = id;
+    }
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      const float xi = my_id[q] >= 0 ? load_logit<DT>(r.logits, t * r.ldl + my_id[q]) : kNegInf;
+      my_w[q] = score64(softmax, xi, (double)top, z);
+    }
+    rank0 = lane;
+  }
+
+  // ---- weights: over their sum where asked (0 where that is 0), times the factor
+  double sum = 0.0;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
-    w[q] = score(my_x[q]);
-    sum += w[q];
+    const int j = q == 0 ? rank0 : q * L + lane;
+    if (j >= r.k) my_w[q] = 0.0;   // a candidate that lost
+    sum += my_w[q];
   }
+  double factor = (double)r.scale;
   if (r.renormalize) {
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor(sum, o, L);
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) w[q] = sum > 0.0 ? w[q] / sum : 0.0;
+    sum = lanes_sum<L>(sum);
+    factor = sum > 0.0 ? factor / sum : 0.0;
   }
   if (token >= r.T) return;
 #pragma unroll
   for (int q = 0; q < kSlots; ++q) {
-    const int j = q * L + lane;
+    const int j = q == 0 ? rank0 : q * L + lane;
     if (j >= r.k) continue;
     r.ids[t * r.k + j] = my_id[q];
-    r.weights[t * r.k + j] = broken ? __builtin_nanf("") : (float)(w[q] * (double)r.scale);
+    r.weights[t * r.k + j] = broken ? __builtin_nanf("") : (float)(my_w[q] * factor);
   }
 }
 
@@ -208,12 +489,21 @@ hipError_t launch_route_shape(const RouteArgs& r, hipStream_t st) {
   return hipGetLastError();
 }
 
+// 16 lanes per token while a lane then holds at most 16 logits: a round's reductions serve four
+// tokens of a wave at once.  Few tokens take a wave each instead: shorter chains.
 template <int DT>
 hipError_t launch_route_type(const RouteArgs& r, hipStream_t st) {
-  if (r.E <= 64) return launch_route_shape<DT, 16, 4>(r, st);
-  if (r.E <= 128) return launch_route_shape<DT, 16, 8>(r, st);
-  if (r.E <= 256) return launch_route_shape<DT, 16, 16>(r, st);
-  if (r.E <= 512) return launch_route_shape<DT, 32, 16>(r, st);
+  if (r.T <= kRouteWide) {
+    if (r.E <= 64) return launch_route_shape<DT, 64, 1>(r, st);
+    if (r.E <= 128) return launch_route_shape<DT, 64, 2>(r, st);
+    if (r.E <= 256) return launch_route_shape<DT, 64, 4>(r, st);
+    if (r.E <= 512) return launch_route_shape<DT, 64, 8>(r, st);
+  } else {
+    if (r.E <= 64) return launch_route_shape<DT, 16, 4>(r, st);
+    if (r.E <= 128) return launch_route_shape<DT, 16, 8>(r, st);
+    if (r.E <= 256) return launch_route_shape<DT, 16, 16>(r, st);
+    if (r.E <= 512) return launch_route_shape<DT, 32, 16>(r, st);
+  }
   return launch_route_shape<DT, 64, 16>(r, st);
 }
 

@@ -139,7 +139,7 @@ struct RouteArgs {
   int64_t T, ldl;
   int E, k, score;         // score: 0 softmax, 1 sigmoid
   const float* bias;       // fp32 [E] or null
-  int groups, top_groups, group_score;   // group_score: 0 best choice, 1 sum of the two best
+  int groups, per_group, top_groups, group_score;   // per_group = E / groups; group_score: 0 best choice, 1 sum of the two best
   int renormalize;
   float scale;
   int32_t* ids;            // [T, k]

@@ -950,6 +950,7 @@ static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales
   g.a_rows = a_rows;
   g.gather = gather != 0;
   g.top_k = (int)k;
+  g.top_k_magic = (uint32_t)((uint64_t(1) << 32) / (uint64_t)k + 1);   // top_k = 1 does not use it
   g.w = static_cast<const uint8_t*>(w_codes);
   g.w_scales = static_cast<const float*>(w_scales);
   g.offsets = offsets;
@@ -966,9 +967,10 @@ static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales
 
 const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
   if ((scheme != PQL_FP8_ROW && scheme != PQL_FP8_BLOCK128) || T < 1 || T > pql::kMoeMaxRows || k < 1 ||
-      k > pql::kMoeMaxTopK || E < 1 || E > pql::kMoeMaxExperts || N < 1 || K < 1)
+      k > pql::kMoeMaxTopK || E < 1 || E > pql::kMoeMaxExperts || N < 1 || N > (int64_t(1) << 20) || K < 1 ||
+      K > (int64_t(1) << 20))
     return "";
-  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, gather != 0, T, k, E, K);
+  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, gather != 0, T, k, E, N, K);
 }
 
 pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,

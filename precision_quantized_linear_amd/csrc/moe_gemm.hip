@@ -5,11 +5,15 @@
 // (gather) or p itself.  FP8_BLOCK128: partial products of each 128-wide K-group promoted with
 // s_a[row, g] s_w[e, n / 128, g] in fp32; FP8_ROW: one fp32 sum scaled by s_a[row] s_w[e, n].
 //
-// k_moe_stream: a workgroup owns 32 columns of one expert and walks the expert's rows 16 at a
-// time; the weight is streamed past them, as in the few-token qlinear kernels: 8 waves take the
+// k_moe_stream: a workgroup owns 32 columns of one expert and walks the expert's rows up to 64 at
+// a time; the weight is streamed past them, as in the few-token qlinear kernels: 8 waves take the
 // K-chunks (128 bytes) round-robin, feed 16x16x128 MFMAs straight from registers, and add
-// their sums in LDS.
+// their sums in LDS.  Bound by the weight stream.  With fewer assignments than experts the grid has one row of
+// workgroups per assignment, and a workgroup finds the experts that have any by ballots over
+// the offsets (a workgroup per expert would be mostly empty ones: 8 of 128 for one token).
+// The first weight loads go out before the rows are looked up: they depend on the expert alone.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.hpp"
 #include "moe_gemm.hpp"
@@ -23,17 +27,39 @@ namespace {
 using namespace gemm;
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kBatch = 3;
 constexpr int kCols = 32;
 
 typedef float v4f_t __attribute__((ext_vector_type(4)));
 
-template <bool ROW>
-__global__ __launch_bounds__(kThreads) void k_moe_stream(MoeGemmArgs g) {
-  __shared__ float part[kWaves][16][kCols + 1];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+// The expert of grid row `slot`: the slot-th with any assignment, or -1.
+__device__ __forceinline__ int active_expert(const MoeGemmArgs& g, int slot, int lane) {
+  int before = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int lo = 0, hi = 0;
+    if (e0 + lane < g.E) expert_range(g, e0 + lane, lo, hi);
+    const uint64_t any = __ballot(hi > lo);
+    const int n = __popcll(any);
+    if (slot < before + n) {   // the (slot - before)-th set bit
+      const uint64_t rank_hit = __ballot((any >> lane & 1) && __popcll(any & ((uint64_t(1) << lane) - 1)) == slot - before);
+      return e0 + __ffsll((unsigned long long)rank_hit) - 1;
+    }
+    before += n;
+  }
+  return -1;
+}
+
+// MAXB: row blocks of 16 a pass may take; EU: waves per SIMD the registers are kept to.  A wave has
+// one K-chunk in flight at a time and many waves run instead: with two or three chunks per wave
+// and half the waves the one-token case (8 experts, N = 2048, K = 4096) takes 14.4 and 15.9 us
+// instead of 13.6, 37 tokens x 6 of 64 experts (N = 2816, K = 2048) 58 and 80 instead of 56.
+template <bool ROW, int MAXB, int EU>
+__global__ __launch_bounds__(kThreads, EU) void k_moe_stream(MoeGemmArgs g) {
+  __shared__ float part[kWaves][MAXB * 16][kCols + 1];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  const int e = blockIdx.y;
+  const int e = __builtin_amdgcn_readfirstlane((int)gridDim.y < g.E ? active_expert(g, blockIdx.y, lane) : (int)blockIdx.y);
+  if (e < 0) return;
   int lo, hi;
   expert_range(g, e, lo, hi);
   if (lo == hi) return;
@@ -42,65 +68,79 @@ __global__ __launch_bounds__(kThreads) void k_moe_stream(MoeGemmArgs g) {
   const uint8_t* wrow[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    wrow[j] = g.w + ((int64_t)e * g.N + std::min<int64_t>(n0 + 16 * j + r16, g.N - 1)) * g.K;
+    wrow[j] = g.w + ((int64_t)e * g.N + std::min<int64_t>(n0 + 16 * j + r16, g.N - 1)) * g.K + 16 * q4;
   const float* swb = g.w_scales + (ROW ? (int64_t)e * g.N : ((int64_t)e * (g.N / 128) + n0 / 128) * nk);
 
-  for (int m0 = lo; m0 < hi; m0 += 16) {
-    const int64_t row = a_row(g, std::min(m0 + r16, hi - 1));
-    const uint8_t* arow = g.a + row * g.K;
-    const float* sarow = g.a_scales + row * (ROW ? 1 : nk);
-    v4f_t acc[2] = {v4f_t{0.f, 0.f, 0.f, 0.f}, v4f_t{0.f, 0.f, 0.f, 0.f}};
-    for (int ck0 = wave; ck0 < nk; ck0 += kWaves * kBatch) {
-      uint4 x[kBatch][2], wv[kBatch][2][2];
-      float sa[kBatch], sw[kBatch];
+  // Up to 16 MB rows from m0 on.
+  auto pass = [&](auto blocks, int m0) __attribute__((always_inline)) {
+    constexpr int MB = decltype(blocks)::value;
+    uint4 wv[2][2];
+    float sw = 0.0f;
+    auto fetch_w = [&](int ck) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int ck = ck0 + u * kWaves;
-        if (ck < nk) {   // wave-uniform
-          const int64_t k0 = (int64_t)ck * 128 + 16 * q4;
-          x[u][0] = ldg16(arow + k0);
-          x[u][1] = ldg16(arow + k0 + 64);
+      for (int j = 0; j < 2; ++j) {
+        wv[j][0] = ldg16(wrow[j] + (int64_t)ck * 128);
+        wv[j][1] = ldg16(wrow[j] + (int64_t)ck * 128 + 64);
+      }
+      if constexpr (!ROW) sw = swb[ck];
+    };
+    fetch_w(std::min(wave, nk - 1));   // a wave without a chunk: unused
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t* arow[MB];
+    const float* sarow[MB];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            wv[u][j][0] = ldg16(wrow[j] + k0);
-            wv[u][j][1] = ldg16(wrow[j] + k0 + 64);
-          }
-          if constexpr (!ROW) {
-            sa[u] = sarow[ck];
-            sw[u] = swb[ck];
-          }
-        }
+    for (int b = 0; b < MB; ++b) {
+      const int64_t row = a_row(g, std::min(m0 + 16 * b + r16, hi - 1));
+      arow[b] = g.a + row * g.K + 16 * q4;
+      sarow[b] = g.a_scales + row * (ROW ? 1 : nk);
+    }
+    v4f_t acc[MB][2];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[b][j] = v4f_t{0.f, 0.f, 0.f, 0.f};
+    for (int ck = wave; ck < nk; ck += kWaves) {
+      uint4 x[MB][2];
+      float sa[MB];
+      if (ck != wave) fetch_w(ck);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        x[b][0] = ldg16(arow[b] + (int64_t)ck * 128);
+        x[b][1] = ldg16(arow[b] + (int64_t)ck * 128 + 64);
+        if constexpr (!ROW) sa[b] = sarow[b][ck];
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (ck0 + u * kWaves >= nk) continue;
-        const v8i qa = cat(x[u][0], x[u][1]);
+      for (int b = 0; b < MB; ++b) {
+        const v8i qa = cat(x[b][0], x[b][1]);
         if constexpr (ROW) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qa, cat(wv[u][j][0], wv[u][j][1]), acc[j], 0, 0,
-                                                                      0, 127, 0, 127);
+            acc[b][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qa, cat(wv[j][0], wv[j][1]), acc[b][j], 0, 0, 0,
+                                                                        127, 0, 127);
         } else {
           float sr[4];   // the lane's outputs are rows 4 q4 + r, whose scales sit in lanes 4 q4 + r
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sr[r] = __shfl(sa[u], 4 * q4 + r);
+          for (int r = 0; r < 4; ++r) sr[r] = __shfl(sa[b], 4 * q4 + r);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const v4f_t P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                qa, cat(wv[u][j][0], wv[u][j][1]), v4f_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+                qa, cat(wv[j][0], wv[j][1]), v4f_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[j][r] = __builtin_fmaf(P[r], sr[r] * sw[u], acc[j][r]);
+            for (int r = 0; r < 4; ++r) acc[b][j][r] = __builtin_fmaf(P[r], sr[r] * sw, acc[b][j][r]);
           }
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][4 * q4 + r][16 * j + r16] = acc[j][r];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave][16 * b + 4 * q4 + r][16 * j + r16] = acc[b][j][r];
     __syncthreads();
-    {
-      const int m = t / kCols, col = t % kCols;   // 512 threads, 16 x 32 outputs
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {   // 512 threads, 16 x 32 outputs of a row block
+      const int m = 16 * b + t / kCols, col = t % kCols;
       const int64_t n = n0 + col;
       float v = 0.0f;
 #pragma unroll
@@ -110,37 +150,77 @@ __global__ __launch_bounds__(kThreads) void k_moe_stream(MoeGemmArgs g) {
         g.c[(int64_t)(m0 + m) * g.ldc + n] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
       }
     }
-    __syncthreads();
+  };
+  for (int m0 = lo; m0 < hi;) {
+    if (m0 != lo) __syncthreads();
+    const int left = hi - m0;
+    if constexpr (MAXB >= 4) {
+      if (left > 32) {
+        pass(std::integral_constant<int, 4>{}, m0);
+        m0 += 64;
+        continue;
+      }
+    }
+    if constexpr (MAXB >= 4) {
+      if (left > 16) {
+        pass(std::integral_constant<int, 2>{}, m0);
+        m0 += 32;
+        continue;
+      }
+    }
+    pass(std::integral_constant<int, 1>{}, m0);
+    m0 += 16;
   }
 }
 
 }  // namespace
 
-// Rows per tile, or 0 for the streaming kernel.
-static int tile_rows(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t K) {
-  // gathered rows are addressed with 32-bit offsets from the activation's start
-  if (gather && a_rows * K > int64_t(0xFFFF0000)) return 0;
-  const int64_t per = P / E;   // rows per expert, were they spread evenly
-  if (per < 24) return 0;
-  return per < 96 ? 64 : per < 384 ? 128 : 256;
+// Which kernel, from the sizes alone (the groups' sizes stay on the device): rows per tile, or
+// minus the row blocks of a streaming pass.  Times in us with block-128 scales, evenly routed:
+//   rows per expert          2      4      8     16     32     64    128
+//   E = 64, N = 4096, K = 2048 (1024 tiles and more)
+//     stream, 1 block       62     76    106    154    256
+//     tiles of 128          77     97    100    104    114
+//   E = 16, N = 2816, K = 2048 (176 tiles)
+//     stream, 1 / 4 blocks  17     --     21     31     43     69    120
+//     tiles of 128          20     --     26     26     27     30     37
+//   E = 8, N = 1024, K = 1024 (32 tiles)
+//     stream, 1 / 4 blocks 4.2    4.3    4.8    5.6    7.5   11.5   20.8
+//     tiles of 128          11     11     11     11     13     16     17
+// A tile reads a weight once for 128 rows; the stream reads it once per pass (16 or 64 rows), but
+// spreads an expert over N / 32 workgroups, so it holds on longer where tiles leave CUs idle.
+// Tiles of 256 rows read the weight half as often and win where both shapes fill the chip (65536
+// rows, 64 experts, N = 4096, K = 2048: 714 against 807; 16 experts of 128 rows, N = 2816: 41 against 37).
+static int kernel_choice(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t N, int64_t K) {
+  const int64_t active = std::min(P, E), per = P / active, tiles_n = (N + 255) / 256;
+  const int64_t tiles = (P / 128 + active) * tiles_n;
+  if (per < 6) return -1;
+  // gathered rows of a tile are addressed with 32-bit offsets from the activation's start
+  if (per < 2048 / tiles || (gather && a_rows * K > int64_t(0xFFFF0000))) return per <= 8 ? -1 : -4;
+  return per >= 32 && (P / 256 + active) * tiles_n >= 512 ? 256 : 128;
 }
 
-hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st) {
-  const int bm = tile_rows(g.P, g.E, g.gather, g.a_rows, g.K);
-  if (bm) return launch_moe_tile(row_scales, bm, g, st);
-  const dim3 grid((unsigned)((g.N + kCols - 1) / kCols), (unsigned)g.E);
-  if (row_scales) hipLaunchKernelGGL(k_moe_stream<true>, grid, dim3(kThreads), 0, st, g);
-  else hipLaunchKernelGGL(k_moe_stream<false>, grid, dim3(kThreads), 0, st, g);
+template <bool ROW>
+static hipError_t launch_stream(int blocks, const MoeGemmArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)((g.N + kCols - 1) / kCols), (unsigned)std::min(g.E, g.P));
+  if (blocks == 1) hipLaunchKernelGGL((k_moe_stream<ROW, 1, 6>), grid, dim3(kThreads), 0, st, g);
+  else hipLaunchKernelGGL((k_moe_stream<ROW, 4, 3>), grid, dim3(kThreads), 0, st, g);
   return hipGetLastError();
 }
 
-const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t K) {
-  switch (tile_rows(T * k, E, gather, gather ? T : T * k, K)) {
-    case 64: return row_scales ? "k_moe_tile<64, fp8_row>" : "k_moe_tile<64, fp8_block128>";
+hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st) {
+  const int c = kernel_choice(g.P, g.E, g.gather, g.a_rows, g.N, g.K);
+  if (c > 0) return launch_moe_tile(row_scales, c, g, st);
+  return row_scales ? launch_stream<true>(-c, g, st) : launch_stream<false>(-c, g, st);
+}
+
+const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+  switch (kernel_choice(T * k, E, gather, gather ? T : T * k, N, K)) {
+    case -1: return row_scales ? "k_moe_stream<1, fp8_row>" : "k_moe_stream<1, fp8_block128>";
+    case -4: return row_scales ? "k_moe_stream<4, fp8_row>" : "k_moe_stream<4, fp8_block128>";
     case 128: return row_scales ? "k_moe_tile<128, fp8_row>" : "k_moe_tile<128, fp8_block128>";
-    case 256: return row_scales ? "k_moe_tile<256, fp8_row>" : "k_moe_tile<256, fp8_block128>";
   }
-  return row_scales ? "k_moe_stream<fp8_row>" : "k_moe_stream<fp8_block128>";
+  return row_scales ? "k_moe_tile<256, fp8_row>" : "k_moe_tile<256, fp8_block128>";
 }
 
 }  // namespace pql

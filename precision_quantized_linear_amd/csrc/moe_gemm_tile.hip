@@ -1,7 +1,8 @@
-// Grouped FP8 products for experts with many rows, gfx950 (tiles of BM rows by 256 columns).
+// Grouped FP8 products for experts with more than a few rows, gfx950 (tiles of BM rows by 256
+// columns).
 //
-// The mathematics is moe_gemm.hip's.  A tile belongs to one expert: BM = 64, 128 or 256 of its
-// rows and 256 of its columns.  8 waves, two per SIMD, as 2 x 4: wave w owns the (BM / 2) x 64
+// The mathematics is moe_gemm.hip's.  A tile belongs to one expert: BM = 128 or 256 of its rows
+// and 256 of its columns.  8 waves, two per SIMD, as 2 x 4: wave w owns the (BM / 2) x 64
 // part (w / 4, w % 4), as MI x 2 blocks of v_mfma_scale_f32_32x32x64_f8f6f4 with unit scales,
 // the W fragment first, so lane l of a block holds row l % 32 and four quads of consecutive
 // columns.  FP8_BLOCK128: a K-group's partial product is promoted into the fp32 sums with one
@@ -24,6 +25,7 @@
 // in LDS, and takes tiles XCD by XCD, expert by expert, in 4-tile-tall column walks, so that
 // workgroups of an XCD share an expert's weight rows in its L2.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.hpp"
 #include "moe_gemm.hpp"
@@ -57,7 +59,8 @@ struct Shape {
   static constexpr int kScales = kSlots * kRegion;
   static constexpr int kEpi = kScales + kSlots * (kSaBytes + 2 * kSwBytes);
   static constexpr int kPrefix = kEpi + kWaves * kEpiBytes;
-  static constexpr int kLds = kPrefix + 4 * (kMoeMaxExperts + 4);
+  static constexpr int kTiles = kPrefix + 4 * (kMoeMaxExperts + 4);
+  static constexpr int kLds = kTiles + 64 * 8;
   static_assert(kLds <= 160 * 1024, "a CU has 160 KB of LDS");
 };
 
@@ -101,43 +104,47 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   const int my_tiles = __builtin_amdgcn_readfirstlane(sched.count);
   if (my_tiles == 0) return;
 
-  // Tile k of this workgroup: its expert, first row, first column and the end of the expert's rows.
+  // The workgroup's tiles, 64 at a time in LDS: entry i holds tile tile_base + i as its first
+  // row, and expert, column tile and live rows packed.
   struct Tile {
-    int e, m0, hi, n0;
+    int e, m0, rows, n0;   // rows: those of the expert from m0 on, at most BM
   };
-  auto tile_at = [&](int k) __attribute__((always_inline)) {
-    const int L = sched.first + k * sched.stride;
-    int e = -1;   // the last expert whose tiles start at or before L
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int i = std::min(e0 + lane, g.E);
-      const uint64_t before = __ballot(e0 + lane < g.E && prefix[i] * tiles_n <= L);
-      e += __popcll(before);
-      if (before != ~uint64_t(0)) break;
+  int* const tiles = reinterpret_cast<int*>(smem + S::kTiles);
+  int tile_base = 0;
+  auto fill_tiles = [&](int base) __attribute__((always_inline)) {
+    tile_base = base;
+    if (wave != 0) return;
+    const int el = fresh_lane();
+    const int L = sched.first + std::min(base + el, my_tiles - 1) * sched.stride;
+    int e = 0, above = g.E;   // prefix[e] * tiles_n <= L < prefix[above] * tiles_n
+    while (above - e > 1) {
+      const int mid = (e + above) >> 1;
+      if (prefix[mid] * tiles_n <= L) e = mid;
+      else above = mid;
     }
-    e = __builtin_amdgcn_readfirstlane(e);
-    const int first = __builtin_amdgcn_readfirstlane(prefix[e]);
     int lo, hi;
     expert_range(g, e, lo, hi);
     const int tiles_m = (hi - lo + S::BM - 1) / S::BM;
-    const int l = L - first * tiles_n;
+    const int l = L - prefix[e] * tiles_n;
     constexpr int kGroupM = 4;
     const int group = l / (kGroupM * tiles_n);
-    const int first_m = group * kGroupM;
-    const int gm = std::max(1, std::min(tiles_m - first_m, kGroupM));
+    const int gm = std::max(1, std::min(tiles_m - group * kGroupM, kGroupM));
     const int r = l - group * kGroupM * tiles_n;
-    Tile tl;
-    tl.e = e;
-    tl.m0 = __builtin_amdgcn_readfirstlane(lo + (first_m + r % gm) * S::BM);
-    tl.hi = __builtin_amdgcn_readfirstlane(hi);
-    tl.n0 = __builtin_amdgcn_readfirstlane((r / gm) * BN);
-    return tl;
+    const int m0 = lo + (group * kGroupM + r % gm) * S::BM;
+    tiles[2 * el] = m0;
+    tiles[2 * el + 1] = (e * 4096 + r / gm) * 512 + std::max(0, std::min(S::BM, hi - m0));
   };
+  auto tile_at = [&](int k) __attribute__((always_inline)) {
+    const int i = 2 * ((k - tile_base) & 63);
+    const int m0 = __builtin_amdgcn_readfirstlane(tiles[i]);
+    const int rest = __builtin_amdgcn_readfirstlane(tiles[i + 1]);
+    return Tile{(int)((uint32_t)rest >> 21), m0, rest & 511, ((rest >> 9) & 4095) * BN};
+  };
+  fill_tiles(0);
+  __syncthreads();
 
   // ---- load stream (see the file comment).  Load p of a wave covers activation rows
   // 8 MI w + 8 p .. + 7 and weight rows 32 w + 8 p .. + 7 of the tile, whole 128-byte lines.
-  int voff_w[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) voff_w[p] = (wave * 32 + 8 * p + (lane >> 3)) * Kb + (dma_chunk(lane, p & 1) << 4);
   struct Cursor {
     v4i a, w, sa, sw;   // descriptors of the tile's codes and scales
     uint32_t voff_a[MI];
@@ -147,36 +154,51 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   // block-128: waves 0 .. MI - 1 load the activation scales of 64 rows each, waves 4 and 6 the
   // weight scales of the tile's two 128-column blocks
   const bool sa_wave = !ROW && wave < MI, sw_wave = !ROW && (wave == 4 || wave == 6);
-  auto cursor_tile = [&](int k) __attribute__((always_inline)) {
-    const Tile tl = tile_at(std::min(k, my_tiles - 1));
-    const int64_t base = g.gather ? 0 : (int64_t)tl.m0;   // gathered rows are offset from the operand's start
-    const uint64_t rows = g.gather ? (uint64_t)g.a_rows : (uint64_t)std::min(S::BM, tl.hi - tl.m0);
-    auto row_of = [&](int m) __attribute__((always_inline)) {   // the row (from base) of tile row m, inside the operand
-      if (!g.gather) return (uint32_t)m;
-      const uint32_t tok = (uint32_t)std::max(g.order[std::min(tl.m0 + m, tl.hi - 1)], 0) / (uint32_t)g.top_k;
-      return std::min<uint32_t>(tok, (uint32_t)g.a_rows - 1);
-    };
-    const int live = tl.hi - tl.m0;
-#pragma unroll
-    for (int p = 0; p < MI; ++p) {
-      const int m = wave * 8 * MI + 8 * p + (lane >> 3);
-      const int odd = MI == 1 ? (wave & 1) : (p & 1);   // parity of the 8-row group
-      cur.voff_a[p] = m < live ? row_of(m) * (uint32_t)Kb + (uint32_t)(dma_chunk(lane, odd) << 4) : kOutside;
-    }
-    const int64_t n = (int64_t)tl.e * g.N + tl.n0;
-    const int nr = (int)std::min<int64_t>(BN, g.N - tl.n0);
+  // The cursor moves to a tile in two steps: start_tile sets the descriptors and, for gathered
+  // rows, issues the loads of the plan's order; finish_tile turns those into offsets, a region
+  // later, when they have landed behind that region's products.
+  bool started = false;
+  Tile ct;
+  auto start_tile = [&](int k) __attribute__((always_inline)) {
+    cur.k = k;
+    cur.rg = 0;
+    ct = tile_at(std::min(k, my_tiles - 1));
+    const int64_t base = g.gather ? 0 : (int64_t)ct.m0;   // gathered rows are offset from the operand's start
+    const uint64_t rows = g.gather ? (uint64_t)g.a_rows : (uint64_t)ct.rows;
+    const int64_t n = (int64_t)ct.e * g.N + ct.n0;
+    const int nr = (int)std::min<int64_t>(BN, g.N - ct.n0);
     cur.a = make_rsrc(g.a + base * Kb, (int)(uint32_t)(rows * (uint64_t)Kb));
     cur.w = make_rsrc(g.w + n * Kb, nr * Kb);
     if constexpr (!ROW) {
-      const int m = (wave & (MI - 1)) * 64 + lane;
-      cur.voff_sa = m < live ? row_of(m) * (uint32_t)(G * 4) : kOutside;
       // the wave's weight block; a wave wholly past N takes the last one (its sums are never stored)
-      const int nb = std::min(tl.n0 / 128 + (wn >> 1), nblocks - 1);
+      const int nb = std::min(ct.n0 / 128 + (wn >> 1), nblocks - 1);
       cur.sa = make_rsrc(g.a_scales + base * G, (int)(uint32_t)(rows * (uint64_t)(G * 4)));
-      cur.sw = make_rsrc(g.w_scales + ((int64_t)tl.e * nblocks + nb) * G, G * 4);
+      cur.sw = make_rsrc(g.w_scales + ((int64_t)ct.e * nblocks + nb) * G, G * 4);
     }
-    cur.k = k;
-    cur.rg = 0;
+    auto row_of = [&](int m) __attribute__((always_inline)) {
+      if (!g.gather) return (uint32_t)m;
+      return (uint32_t)g.order[ct.m0 + std::max(0, std::min(m, ct.rows - 1))];
+    };
+#pragma unroll
+    for (int p = 0; p < MI; ++p) cur.voff_a[p] = row_of(wave * 8 * MI + 8 * p + (lane >> 3));
+    if constexpr (!ROW) cur.voff_sa = row_of((wave & (MI - 1)) * 64 + lane);
+    started = true;
+  };
+  auto finish_tile = [&]() __attribute__((always_inline)) {
+    auto row_of = [&](uint32_t raw) __attribute__((always_inline)) {   // inside the operand, whatever the order holds
+      return g.gather ? token_of(g, (int32_t)raw) : raw;
+    };
+#pragma unroll
+    for (int p = 0; p < MI; ++p) {
+      const int m = wave * 8 * MI + 8 * p + (lane >> 3);
+      const uint32_t off = row_of(cur.voff_a[p]) * (uint32_t)Kb + (uint32_t)(dma_chunk(lane, p & 1) << 4);
+      cur.voff_a[p] = m < ct.rows ? off : kOutside;
+    }
+    if constexpr (!ROW) {
+      const int m = (wave & (MI - 1)) * 64 + lane;
+      cur.voff_sa = m < ct.rows ? row_of(cur.voff_sa) * (uint32_t)(G * 4) : kOutside;
+    }
+    started = false;
   };
   uint8_t* const sa_lds = smem + S::kScales;                            // [slot][BM] floats
   uint8_t* const sw_lds = sa_lds + S::kSlots * S::kSaBytes;             // [slot][block][64] floats
@@ -188,6 +210,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   auto issue = [&](int slot) __attribute__((always_inline)) {
     uint8_t* const base = smem + slot * S::kRegion;
     const int so = cur.rg * kRow;
+    // weight rows 8 apart differ by 8 K bytes and the parity bit of the swizzle; formed afresh,
+    // as the fragments' addresses are: kept, they would cost registers that the sums need
+    const int fl = fresh_lane();
+    const int voff_w = (wave * 32 + (fl >> 3)) * Kb + (dma_chunk(fl, 0) << 4);
     if constexpr (!ROW) {   // the scales first: a gather, one cache line per row
       if (sa_wave) lds_load4_so(cur.sa, sa_lds + slot * S::kSaBytes + wave * 256, (int)cur.voff_sa, cur.rg * 4);
       if (sw_wave) lds_load4_so(cur.sw, sw_lds + (slot * 2 + (wn >> 1)) * S::kSwBytes, 0, cur.rg * 4);
@@ -197,21 +223,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
       lds_load16_so(cur.a, base + (wave * 8 * MI + 8 * p) * kRow, (int)cur.voff_a[p], so);
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-      lds_load16_so(cur.w, base + S::kAOp + (wave * 32 + 8 * p) * kRow, voff_w[p], so);
-    if (++cur.rg == G) cursor_tile(cur.k + 1);
+      lds_load16_so(cur.w, base + S::kAOp + (wave * 32 + 8 * p) * kRow, (voff_w ^ ((p & 1) << 6)) + 8 * p * Kb, so);
+    if (++cur.rg == G) start_tile(cur.k + 1);
   };
 
   // ---- fragments: 32x32x64 operands, lane row l % 32; slice h takes chunks 4 h + c and
   // 4 h + 2 + c (c = l / 32) of the row; rows + 32 i keep the swizzle.
-  const int r32 = lane & 31, c32 = lane >> 5;
-  int a_off[2][2], w_off[2][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      a_off[h][q] = swz128(wm * 32 * MI + r32, 4 * h + 2 * q + c32);
-      w_off[h][q] = S::kAOp + swz128(wn * 64 + r32, 4 * h + 2 * q + c32);
-    }
+  // Wave (wm, wn) takes row blocks wm, wm + 2, ..: a tile with few live rows then leaves both
+  // waves of a SIMD about the same work.
+  int a_base, w_base;
   uint4 fw[2][2][2];   // [j][slice][chunk]
   uint4 fa[2][2][2];   // [buffer][slice][chunk]: A block i in buffer i % 2
   auto read_w = [&](const uint8_t* region) __attribute__((always_inline)) {
@@ -220,20 +240,20 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) fw[j][h][q] = lds16(region + w_off[h][q] + j * 32 * kRow);
+        for (int q = 0; q < 2; ++q) fw[j][h][q] = lds16(region + (w_base ^ (h * 64 + q * 32)) + j * 32 * kRow);
   };
   auto read_a = [&](const uint8_t* region, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) fa[i & 1][h][q] = lds16(region + a_off[h][q] + i * 32 * kRow);
+      for (int q = 0; q < 2; ++q) fa[i & 1][h][q] = lds16(region + (a_base ^ (h * 64 + q * 32)) + i * 64 * kRow);
   };
-  float sc[MI], last_sc = 0.f;   // s_a * s_w per 32-row block: this region's; the previous region's last
-  auto read_scales = [&](int slot) __attribute__((always_inline)) {
-    const float* sa = reinterpret_cast<const float*>(sa_lds + slot * S::kSaBytes) + wm * 32 * MI + r32;
-    const float sw = reinterpret_cast<const float*>(sw_lds + (slot * 2 + (wn >> 1)) * S::kSwBytes)[lane];
+  float sc[MI];   // s_a * s_w per 32-row block of this region
+  auto read_scales = [&](int slot, int fl) __attribute__((always_inline)) {
+    const float* sa = reinterpret_cast<const float*>(sa_lds + slot * S::kSaBytes) + wm * 32 + (fl & 31);
+    const float sw = reinterpret_cast<const float*>(sw_lds + (slot * 2 + (wn >> 1)) * S::kSwBytes)[fl];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) sc[i] = sa[i * 32] * sw;
+    for (int i = 0; i < MI; ++i) sc[i] = sa[i * 64] * sw;
   };
 
   v16f acc[MI][2];
@@ -242,34 +262,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[b >> 1][b & 1][e] = __builtin_fmaf(P[b & 1][e], s, acc[b >> 1][b & 1][e]);
   };
-  auto region = [&](int slot, int next_slot, bool carry) __attribute__((always_inline)) {
-    const uint8_t* rgn = smem + slot * S::kRegion;
-    issue(next_slot);
-    read_w(rgn);
-    read_a(rgn, 0);
-    if constexpr (!ROW) {
-      if (carry) last_sc = sc[MI - 1];
-      read_scales(slot);
-      if (carry) promote(2 * MI - 1, last_sc);
+  // The two MFMAs of block b.
+  auto block = [&](int b) __attribute__((always_inline)) {
+    const int i = b >> 1, j = b & 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const v8i w8 = cat(fw[j][h][0], fw[j][h][1]), a8 = cat(fa[i & 1][h][0], fa[i & 1][h][1]);
+      if constexpr (ROW)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc[i][j], 0, 0, 0, 127, 0, 127);
+      else
+        P[b & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, h ? P[b & 1] : v16f{}, 0, 0, 0, 127, 0, 127);
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int b = 0; b < 2 * MI; ++b) {
-      const int i = b >> 1, j = b & 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v8i w8 = cat(fw[j][h][0], fw[j][h][1]), a8 = cat(fa[i & 1][h][0], fa[i & 1][h][1]);
-        if constexpr (ROW)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc[i][j], 0, 0, 0, 127, 0, 127);
-        else
-          P[b & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, h ? P[b & 1] : v16f{}, 0, 0, 0, 127, 0, 127);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (j == 0 && i + 1 < MI) read_a(rgn, i + 1);
+  };
+  // A region of a tile in which LIVE of this wave's row blocks hold rows: a block's promotion
+  // runs behind the next block's MFMAs, the last one's behind the next region's first (carry).
+  auto region = [&](auto live_c, const uint8_t* rgn, int slot) __attribute__((always_inline)) {
+    constexpr int LIVE = decltype(live_c)::value;
+    if constexpr (LIVE > 0) {
+      const int fl = fresh_lane();
+      a_base = swz128(wm * 32 + (fl & 31), fl >> 5);
+      w_base = S::kAOp + swz128(wn * 64 + (fl & 31), fl >> 5);
+      read_w(rgn);
+      read_a(rgn, 0);
       if constexpr (!ROW) {
-        if (b > 0) promote(b - 1, sc[(b - 1) >> 1]);
+        promote(2 * LIVE - 1, sc[LIVE - 1]);   // the previous region's (a tile starts with P = 0)
+        read_scales(slot, fl);
       }
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < 2 * LIVE; ++b) {
+        const int i = b >> 1, j = b & 1;
+        block(b);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0 && i + 1 < LIVE) read_a(rgn, i + 1);
+        if constexpr (!ROW) {
+          if (b > 0) promote(b - 1, sc[(b - 1) >> 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
 
@@ -278,9 +308,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   // lane 8 consecutive columns; where rows of C start on 16 bytes and the wave's 64 columns
   // exist they are staged 8 rows at a time (16-byte piece c of row r at c ^ r) and written as
   // whole 128-byte row segments.
-  auto epilogue = [&](int k) __attribute__((always_inline)) {
-    const Tile tl = tile_at(k);
-    const int m0 = tl.m0 + wm * 32 * MI;
+  auto epilogue = [&](auto live_c, const Tile& tl) __attribute__((always_inline)) {
+    constexpr int LIVE = decltype(live_c)::value;
+    const int m0 = tl.m0 + wm * 32, hi = tl.m0 + tl.rows;
     const int64_t n0 = tl.n0 + wn * 64;
     const bool staged = g.vec_store && n0 + 64 <= g.N;   // wave-uniform
     const int el = fresh_lane();
@@ -295,10 +325,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
         for (int q = 0; q < 16; ++q) cs[j][q] = sw[std::min<int64_t>(n0 + j * 32 + (q >> 2) * 8 + fk * 4 + (q & 3), g.N - 1)];
     }
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (m0 + i * 32 >= tl.hi) break;     // wave-uniform
+    for (int i = 0; i < LIVE; ++i) {
       float rs = 1.0f;
-      if constexpr (ROW) rs = g.a_scales[a_row(g, std::min(m0 + i * 32 + fr, tl.hi - 1))];
+      if constexpr (ROW) rs = g.a_scales[a_row(g, std::min(m0 + i * 64 + fr, hi - 1))];
       uint4 u[2][2];   // [j][h]
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -332,12 +361,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
           asm volatile("" ::: "memory");
           const uint4 w = lds16(epi + rr * 128 + ((rc ^ rr) << 4));
           asm volatile("" ::: "memory");
-          const int row = m0 + i * 32 + 8 * p + rr;
-          if (row < tl.hi) *reinterpret_cast<uint4*>(g.c + (int64_t)row * g.ldc + n0 + rc * 8) = w;
+          const int row = m0 + i * 64 + 8 * p + rr;
+          if (row < hi) __builtin_nontemporal_store(__builtin_bit_cast(v4i, w), reinterpret_cast<v4i*>(g.c + (int64_t)row * g.ldc + n0 + rc * 8));
         }
       } else {
-        const int row = m0 + i * 32 + fr;
-        if (row < tl.hi) {
+        const int row = m0 + i * 64 + fr;
+        if (row < hi) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -356,33 +385,56 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   };
 
   // ---- the stream
-  cursor_tile(0);
+  start_tile(0);
+  finish_tile();
 #pragma unroll
-  for (int s = 0; s < S::kSlots - 1; ++s) issue(s);
+  for (int s = 0; s < S::kSlots - 1; ++s) {
+    issue(s);
+    if (started) finish_tile();
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) sc[i] = 0.f;
   int slot = 0;
-  for (int k = 0; k < my_tiles; ++k) {
+  auto walk = [&](auto live_c) __attribute__((always_inline)) {   // a tile's K-groups
+    constexpr int LIVE = decltype(live_c)::value;
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < LIVE; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
+    if constexpr (!ROW) P[1] = v16f{};
     for (int r = 0; r < G; ++r) {
-      // this wave's loads of the region (those of the S - 2 regions after it may be in flight)
-      if constexpr (S::kSlots == 2) {
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-      } else if (sa_wave || sw_wave) {
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * (kLoads + 1), 0));
-      } else {
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * kLoads, 0));
-      }
+      // This wave's loads of the region; those of the S - 2 regions after it may be in flight.  (The
+      // last tile's stores are waited for too: letting them run behind the first region, by
+      // counting them, measured 10 % slower over the whole kernel.)
+      if constexpr (S::kSlots == 2) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+      else if (sa_wave || sw_wave) __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * (kLoads + 1), 0));
+      else __builtin_amdgcn_s_waitcnt(waitcnt_imm((S::kSlots - 2) * kLoads, 0));
       __builtin_amdgcn_s_barrier();   // everyone's; the previous region's slot is free
       __builtin_amdgcn_sched_barrier(0);
-      region(slot, slot == 0 ? S::kSlots - 1 : slot - 1, r > 0);
+      if (started) finish_tile();     // (after the region's products it would draw them below its branch)
+      issue(slot == 0 ? S::kSlots - 1 : slot - 1);
+      region(live_c, smem + slot * S::kRegion, slot);
       slot = slot + 1 == S::kSlots ? 0 : slot + 1;
     }
-    if constexpr (!ROW) promote(2 * MI - 1, sc[MI - 1]);   // the tile's last block
-    epilogue(k);
+    if constexpr (!ROW && LIVE > 0) promote(2 * LIVE - 1, sc[LIVE - 1]);   // the tile's last block
+  };
+  for (int k = 0; k < my_tiles; ++k) {
+    // while tile k runs the cursor reads up to tile k + kSlots (one K-group per tile)
+    if (k + S::kSlots >= tile_base + 64) {
+      __syncthreads();   // everyone has read its tiles
+      fill_tiles(k);
+      __syncthreads();
+    }
+    const Tile tl = tile_at(k);
+    const int live = std::max(0, std::min(MI, (tl.rows - wm * 32 + 63) >> 6));
+    using std::integral_constant;
+    switch (live) {
+      case 4: if constexpr (MI == 4) { walk(integral_constant<int, 4>{}); epilogue(integral_constant<int, 4>{}, tl); } break;
+      case 3: if constexpr (MI == 4) { walk(integral_constant<int, 3>{}); epilogue(integral_constant<int, 3>{}, tl); } break;
+      case 2: walk(integral_constant<int, 2>{}); epilogue(integral_constant<int, 2>{}, tl); break;
+      case 1: walk(integral_constant<int, 1>{}); epilogue(integral_constant<int, 1>{}, tl); break;
+      default: walk(integral_constant<int, 0>{});   // its share of the loads
+    }
   }
   __builtin_amdgcn_s_waitcnt(0);
 }
@@ -400,9 +452,8 @@ hipError_t launch_shape(const MoeGemmArgs& g, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_moe_tile(bool row_scales, int bm, const MoeGemmArgs& g, hipStream_t st) {
-  if (row_scales)
-    return bm == 64 ? launch_shape<1, true>(g, st) : bm == 128 ? launch_shape<2, true>(g, st) : launch_shape<4, true>(g, st);
-  return bm == 64 ? launch_shape<1, false>(g, st) : bm == 128 ? launch_shape<2, false>(g, st) : launch_shape<4, false>(g, st);
+  if (row_scales) return bm == 128 ? launch_shape<2, true>(g, st) : launch_shape<4, true>(g, st);
+  return bm == 128 ? launch_shape<2, false>(g, st) : launch_shape<4, false>(g, st);
 }
 
 }  // namespace pql

@@ -163,6 +163,7 @@ struct MoeGemmArgs {
   int64_t a_rows;
   int gather;              // row(p) = order[p] / top_k, else p
   int top_k;
+  uint32_t top_k_magic;    // i / top_k = top_k == 1 ? i : (i * top_k_magic) >> 32 for i < 2^24 (top_k <= 32)
   const uint8_t* w;        // weight codes [E, N, K]
   const float* w_scales;   // [E, N / 128, K / 128] or [E, N]
   const int32_t* offsets;  // [E + 1]
@@ -174,9 +175,9 @@ struct MoeGemmArgs {
   int vec_store;           // 1 if c and ldc allow 16-byte row stores
 };
 hipError_t launch_moe_gemm(bool row_scales, const MoeGemmArgs& g, hipStream_t st);
-// Tiles of bm = 64, 128 or 256 rows (a gathered activation of at most 2^32 - 2^16 bytes).
+// Tiles of bm = 128 or 256 rows (a gathered activation of at most 2^32 - 2^16 bytes).
 hipError_t launch_moe_tile(bool row_scales, int bm, const MoeGemmArgs& g, hipStream_t st);
-const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t K);
+const char* moe_gemm_kernel_name(bool row_scales, bool gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
 
 // Codes and scales of silu(x[:, :F]) * x[:, F:]; rows at and past *count (if given) are left alone.
 hipError_t launch_swiglu_quantize(bool per_row, const uint16_t* x, int64_t rows, int64_t F, int64_t ldx,

@@ -229,7 +229,40 @@ GEMM_CASES = [
     ("fp8_row", 37, 3, 10, 520, 384, "spread"), ("fp8_row", 40, 2, 3, 264, 512, "dropped"),
     ("fp8_row", 300, 2, 5, 33, 256, "crowded"), ("fp8_row", 700, 1, 2, 577, 384, "spread"),
     ("fp8_row", 290, 2, 4, 256, 128, "one"), ("fp8_row", 1100, 3, 4, 712, 512, "spread"),
+    # the 256-row tiles: experts of a few rows to several tiles, columns past the last whole tile
+    ("fp8_block128", 1430, 3, 130, 1024, 384, "spread"), ("fp8_block128", 1350, 2, 9, 8064, 256, "crowded"),
+    ("fp8_row", 1430, 3, 130, 1000, 384, "dropped"), ("fp8_row", 1350, 2, 9, 8190, 256, "crowded"),
 ]
+
+
+def test_gemm_cases_reach_every_kernel():
+    names = {pql.moe_kernel_name(s, T, k, E, N, K, gather) for s, T, k, E, N, K, _ in GEMM_CASES for gather in (0, 1)}
+    assert names == {f"k_moe_{n}, {s}>" for n in ("stream<1", "stream<4", "tile<128", "tile<256")
+                     for s in ("fp8_row", "fp8_block128")}
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+def test_gemm_many_tiles_per_workgroup(scheme):
+    """80 tiles of 256 x 256 per CU (the schedule's table holds 64): exact operands, so the fp32
+    product of the decoded codes and power-of-two scales is exact and every element must equal its bf16
+    rounding."""
+    T, E, N, K = 20000, 2, 65536, 128
+    plan, offsets, order = _grouped("spread", T, 1, E, 5)
+    a, w = exact_operand(scheme, "activation", T, K, 3), exact_operand(scheme, "weight", E * N, K, 4)
+    c = pql.moe_qgemm(pql.from_numpy(a, DEV), pql.from_numpy(w, DEV), plan, gather=True)
+    table = dev(F.e4m3_decode(np.arange(256, dtype=np.uint8)).astype(np.float32))
+
+    def decoded(q, repeat):
+        s = dev(q["scales"]) if q["scales"].ndim == 1 else dev(q["scales"]).repeat_interleave(repeat, 0)
+        return table[dev(q["codes"]).long()] * s.reshape(q["rows"], -1)
+
+    A, W = decoded(a, 1), decoded(w, 128).view(E, N, K)
+    for e in range(E):
+        rows = plan.order[offsets[e]:offsets[e + 1]].long()
+        for at in range(0, len(rows), 2048):
+            want = (A[rows[at:at + 2048]] @ W[e].t()).bfloat16()
+            got = c[int(offsets[e]) + at: int(offsets[e]) + at + want.shape[0]]
+            assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("gather", [True, False])

@@ -539,7 +539,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_count(const int32_t* __res
   for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[(int64_t)blockIdx.x * E + e] = n[e];
 }
 
-// counts: [gridDim.x][E] from k_moe_count; unused by a single workgroup.
+// counts: [gridDim.x][E] from k_moe_count; unused by a single workgroup.  ROUNDS > 0: a wave's
+// part is at most 64 ROUNDS ids, held in registers with their ranks (their loads are then one
+// latency, not two per round); 0: any length, read and ranked twice.
+template <int ROUNDS>
 __global__ __launch_bounds__(kPlanThreads) void k_moe_place(const int32_t* __restrict__ ids, int P, int E, int chunk,
                                                             const int32_t* __restrict__ counts,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ order,
@@ -567,12 +570,26 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_place(const int32_t* __res
     return same;
   };
   // Only this wave touches seen[wave], and LDS runs a wave's accesses in order; the fences
-  // keep the compiler from reordering or merging them across lanes.
-  for (int i0 = begin; i0 < end; i0 += 64) {
-    const int id = id_at(i0 + lane);
+  // keep the compiler from reordering or merging them across lanes.  Returns the rank among the
+  // wave's ids so far.
+  auto count_in = [&](int id) __attribute__((always_inline)) {
     const uint64_t same = lanes_with(id);
+    int rank = 0;
+    if (id < E) rank = seen[wave][id] + __popcll(same & below);
+    asm volatile("" ::: "memory");
     if (id < E && !(same & below)) seen[wave][id] += __popcll(same);
     asm volatile("" ::: "memory");
+    return rank;
+  };
+  constexpr int kHeld = ROUNDS > 0 ? ROUNDS : 1;
+  int held[kHeld], rank[kHeld];
+  if constexpr (ROUNDS > 0) {
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) held[q] = id_at(begin + 64 * q + lane);
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) rank[q] = count_in(held[q]);
+  } else {
+    for (int i0 = begin; i0 < end; i0 += 64) count_in(id_at(i0 + lane));
   }
   __syncthreads();
 
@@ -583,7 +600,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_place(const int32_t* __res
 #pragma unroll
       for (int w = 0; w < kPlanWaves; ++w) all += seen[w][e];
     } else {
-#pragma unroll 8
+#pragma unroll 16
       for (int b = 0; b < (int)gridDim.x; ++b) {
         const int n = counts[(int64_t)b * E + e];
         all += n;
@@ -624,17 +641,23 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_place(const int32_t* __res
   if (blockIdx.x == 0 && t == 0) offsets[E] = total;
   __syncthreads();
 
-  for (int i0 = begin; i0 < end; i0 += 64) {
-    const int i = i0 + lane;
-    const int id = id_at(i);
-    const uint64_t same = lanes_with(id);
-    int place = -1;
-    if (id < E) place = start[id] + seen[wave][id] + __popcll(same & below);
-    asm volatile("" ::: "memory");
-    if (id < E && !(same & below)) seen[wave][id] += __popcll(same);
-    asm volatile("" ::: "memory");
-    if (i < end) slots[i] = place;
-    if (place >= 0) order[place] = i;
+  // seen[wave][e] is now where the wave's first assignment of e goes, from the expert's start on
+  auto put = [&](int i, int id, int place) __attribute__((always_inline)) {
+    if (i < end) slots[i] = id < E ? place : -1;
+    if (id < E) order[place] = i;
+  };
+  if constexpr (ROUNDS > 0) {
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) {
+      const int id = held[q];
+      put(begin + 64 * q + lane, id, id < E ? start[id] + seen[wave][id] + rank[q] : -1);
+    }
+  } else {
+    for (int i0 = begin; i0 < end; i0 += 64) {
+      const int id = id_at(i0 + lane);
+      const int r = count_in(id);
+      put(i0 + lane, id, id < E ? start[id] + r : -1);
+    }
   }
   for (int64_t i = total + (int64_t)blockIdx.x * kPlanThreads + t; i < P; i += (int64_t)gridDim.x * kPlanThreads)
     order[i] = -1;
@@ -661,8 +684,16 @@ hipError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offset
                            int32_t* ws, hipStream_t st) {
   const int blocks = plan_blocks(P), chunk = (int)plan_chunk(P);
   if (blocks > 1) hipLaunchKernelGGL(k_moe_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws);
-  hipLaunchKernelGGL(k_moe_place, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws, offsets, order,
-                     slots);
+  constexpr int kRounds = kPlanChunk / kPlanThreads;
+  if (P <= kPlanThreads)
+    hipLaunchKernelGGL(k_moe_place<1>, dim3(1), dim3(kPlanThreads), 0, st, ids, (int)P, E, kPlanThreads, ws, offsets,
+                       order, slots);
+  else if (chunk == kPlanChunk)
+    hipLaunchKernelGGL(k_moe_place<kRounds>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws,
+                       offsets, order, slots);
+  else
+    hipLaunchKernelGGL(k_moe_place<0>, dim3(blocks), dim3(kPlanThreads), 0, st, ids, (int)P, E, chunk, ws, offsets,
+                       order, slots);
   return hipGetLastError();
 }
 

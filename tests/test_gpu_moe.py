@@ -186,7 +186,7 @@ def check_plan(ids, E):
 
 @pytest.mark.parametrize("T,k,E", [(0, 3, 5), (1, 1, 1), (1, 8, 64), (5, 3, 7), (24, 6, 160), (64, 8, 64), (171, 3, 65),
                                    (512, 1, 2), (513, 2, 1024), (1000, 8, 60), (4096, 8, 256), (9001, 7, 511),
-                                   (30011, 8, 128)])
+                                   (30011, 8, 128), (70001, 8, 100)])
 def test_plan(T, k, E):
     rng = np.random.default_rng(T + E)
     check_plan(rng.integers(0, E, (T, k)), E)

@@ -42,7 +42,6 @@ constexpr int kThreads = 512;
 constexpr int kWaves = 8;
 constexpr int BN = 256;
 constexpr int kRow = 128;                          // bytes of one K-group per row
-constexpr int kEpiBytes = 8 * 128;                 // per wave: 8 staged output rows of 64 bf16
 constexpr int kPersistentCap = 256;
 constexpr uint32_t kOutside = 0xFFFFFFF0u;         // a row offset outside every descriptor
 
@@ -57,8 +56,7 @@ struct Shape {
   static constexpr int kSaBytes = ROW ? 0 : BM * 4;        // activation scales of one group
   static constexpr int kSwBytes = ROW ? 0 : 256;           // a weight block's scale, one copy per lane
   static constexpr int kScales = kSlots * kRegion;
-  static constexpr int kEpi = kScales + kSlots * (kSaBytes + 2 * kSwBytes);
-  static constexpr int kPrefix = kEpi + kWaves * kEpiBytes;
+  static constexpr int kPrefix = kScales + kSlots * (kSaBytes + 2 * kSwBytes);
   static constexpr int kTiles = kPrefix + 4 * (kMoeMaxExperts + 4);
   static constexpr int kLds = kTiles + 64 * 8;
   static_assert(kLds <= 160 * 1024, "a CU has 160 KB of LDS");
@@ -202,7 +200,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   };
   uint8_t* const sa_lds = smem + S::kScales;                            // [slot][BM] floats
   uint8_t* const sw_lds = sa_lds + S::kSlots * S::kSaBytes;             // [slot][block][64] floats
-  uint8_t* const epi = smem + S::kEpi + wave * kEpiBytes;               // this wave's output staging
   // Loads per wave and region, which the waits count: these, and one of scales on some waves.
   constexpr int kLoads = MI + 4;
   // The next region of the stream into `slot` (past the last tile: that tile again, into slots
@@ -305,29 +302,38 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
 
   // ---- epilogue.  In block (i, j) lane (r, c) = (l % 32, l / 32) holds, per register quad rq,
   // columns 8 rq + 4 c .. + 3 of row 32 i + r.  One v_permlane32_swap per packed dword leaves the
-  // lane 8 consecutive columns; where rows of C start on 16 bytes and the wave's 64 columns
-  // exist they are staged 8 rows at a time (16-byte piece c of row r at c ^ r) and written as
-  // whole 128-byte row segments.
+  // lane 8 consecutive columns, and where rows of C start on 16 bytes and the wave's 64 columns
+  // exist a v_permlane16_swap brings four lanes' pieces of a row together: each store writes 64
+  // consecutive bytes of 16 rows.  (Staging whole 128-byte segments in LDS took 7100 of a tile's
+  // 75000 cycles: its writes use a quarter of the lanes at a time, for want of LDS.)
   auto epilogue = [&](auto live_c, const Tile& tl) __attribute__((always_inline)) {
     constexpr int LIVE = decltype(live_c)::value;
     const int m0 = tl.m0 + wm * 32, hi = tl.m0 + tl.rows;
     const int64_t n0 = tl.n0 + wn * 64;
-    const bool staged = g.vec_store && n0 + 64 <= g.N;   // wave-uniform
+    const bool whole = g.vec_store && n0 + 64 <= g.N;   // wave-uniform
     const int el = fresh_lane();
     const int fr = el & 31, fk = el >> 5;
-    const int rr = el >> 3, rc = el & 7;   // staged read-back: row rr, 16-byte piece rc
-    float cs[2][16];                       // FP8_ROW: the scales of the lane's columns
+    float cs[2][16], row_s[LIVE > 0 ? LIVE : 1];   // FP8_ROW: the scales of the lane's columns and rows
     if constexpr (ROW) {
+#pragma unroll
+      for (int i = 0; i < LIVE; ++i) row_s[i] = g.a_scales[a_row(g, std::min(m0 + i * 64 + fr, hi - 1))];
       const float* sw = g.w_scales + (int64_t)tl.e * g.N;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) cs[j][q] = sw[std::min<int64_t>(n0 + j * 32 + (q >> 2) * 8 + fk * 4 + (q & 3), g.N - 1)];
+        for (int rq = 0; rq < 4; ++rq) {
+          const int64_t n = n0 + j * 32 + rq * 8 + fk * 4;
+          if (n0 + 64 <= g.N) {   // wave-uniform
+            __builtin_memcpy(&cs[j][4 * rq], sw + n, 16);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cs[j][4 * rq + q] = sw[std::min<int64_t>(n + q, g.N - 1)];
+          }
+        }
     }
 #pragma unroll
     for (int i = 0; i < LIVE; ++i) {
-      float rs = 1.0f;
-      if constexpr (ROW) rs = g.a_scales[a_row(g, std::min(m0 + i * 64 + fr, hi - 1))];
+      const float rs = ROW ? row_s[i] : 1.0f;
       uint4 u[2][2];   // [j][h]
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -347,22 +353,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
           u[j][h] = uint4{s0[0], s1[0], s0[1], s1[1]};
         }
       }
-      if (staged) {
+      if (whole) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {   // rows 8 p .. + 7 of the block
-          if ((fr >> 3) == p) {
+        for (int j = 0; j < 2; ++j) {
+          uint32_t lo[4], hi4[4];
+          const uint32_t x[4] = {u[j][0].x, u[j][0].y, u[j][0].z, u[j][0].w}, y[4] = {u[j][1].x, u[j][1].y, u[j][1].z, u[j][1].w};
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4*>(epi + (fr & 7) * 128 + (((j * 4 + h * 2 + fk) ^ (fr & 7)) << 4)) = u[j][h];
+          for (int q = 0; q < 4; ++q) {
+            const auto sw2 = __builtin_amdgcn_permlane16_swap(x[q], y[q], false, false);
+            lo[q] = sw2[0];
+            hi4[q] = sw2[1];
           }
-          // rows pass between lanes of the wave (LDS runs one wave's accesses in order)
-          asm volatile("" ::: "memory");
-          const uint4 w = lds16(epi + rr * 128 + ((rc ^ rr) << 4));
-          asm volatile("" ::: "memory");
-          const int row = m0 + i * 64 + 8 * p + rr;
-          if (row < hi) __builtin_nontemporal_store(__builtin_bit_cast(v4i, w), reinterpret_cast<v4i*>(g.c + (int64_t)row * g.ldc + n0 + rc * 8));
+          const int row = m0 + i * 64 + (el & 15), g4 = el >> 4;
+          uint16_t* dst = g.c + (int64_t)row * g.ldc + n0 + j * 32 + ((g4 & 1) * 2 + (g4 >> 1)) * 8;
+          if (row < hi) *reinterpret_cast<uint4*>(dst) = uint4{lo[0], lo[1], lo[2], lo[3]};
+          if (row + 16 < hi) *reinterpret_cast<uint4*>(dst + 16 * g.ldc) = uint4{hi4[0], hi4[1], hi4[2], hi4[3]};
         }
       } else {
         const int row = m0 + i * 64 + fr;

@@ -8,6 +8,10 @@ There is no CPU fallback: if the library is missing, every call raises.
     import precision_quantized_linear_amd as pql
     wq = pql.quantize(w, "mxfp8", "weight")      # once, at load
     y = pql.qlinear(x, wq)                        # every call: quantize x, GEMM
+
+A layer of experts (``moe_route``, ``moe_plan``, ``moe_qgemm``, ``swiglu_quantize``,
+``moe_combine``, and all of them after the router as ``moe_mlp``) is for inference like the
+rest: no call records a gradient.
 """
 from __future__ import annotations
 
@@ -634,7 +638,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     return ids, weights
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _plan_workspace(T: int, k: int, n_experts: int) -> int:
     wsb = ctypes.c_size_t()
     _check(lib().pql_moe_plan_workspace(T, k, n_experts, ctypes.byref(wsb)), "moe_plan")
@@ -745,6 +749,8 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor, add: torc
     N = y.shape[1]
     ldy = _check_rows(y, "y", P, N, device)
     _check_vector(weights, "weights", torch.float32, P, device)
+    if weights.dim() != 2 or weights.shape[0] != T:
+        raise ValueError(f"weights must be [{T}, {plan.top_k}], not {tuple(weights.shape)}")
     ldadd = N if add is None else _check_rows(add, "add", T, N, device)
     if out is None:
         out, ldo = torch.empty((T, N), dtype=torch.bfloat16, device=device), N
@@ -769,7 +775,8 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w_in: QTe
         raise ValueError("the two weights' schemes differ")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError(f"ids must be [{x.shape[0]}, top_k]")
-    plan = moe_plan(ids, n_experts)
-    h = moe_qgemm(quantize(x, w_in.scheme), w_in, plan, gather=True)
-    y = moe_qgemm(swiglu_quantize(h, w_in.scheme, plan), w_out, plan)
-    return moe_combine(y, plan, weights, add=add)
+    with torch.cuda.device(x.device):
+        plan = moe_plan(ids, n_experts)
+        h = moe_qgemm(quantize(x, w_in.scheme), w_in, plan, gather=True)
+        y = moe_qgemm(swiglu_quantize(h, w_in.scheme, plan), w_out, plan)
+        return moe_combine(y, plan, weights, add=add)

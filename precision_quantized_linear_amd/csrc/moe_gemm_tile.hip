@@ -282,7 +282,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
       read_w(rgn);
       read_a(rgn, 0);
       if constexpr (!ROW) {
-        promote(2 * LIVE - 1, sc[LIVE - 1]);   // the previous region's (a tile starts with P = 0)
+          promote(2 * LIVE - 1, sc[LIVE - 1]);   // the previous region's
         read_scales(slot, fl);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -397,8 +397,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
     issue(s);
     if (started) finish_tile();
   }
-#pragma unroll
-  for (int i = 0; i < MI; ++i) sc[i] = 0.f;
   int slot = 0;
   auto walk = [&](auto live_c) __attribute__((always_inline)) {   // a tile's K-groups
     constexpr int LIVE = decltype(live_c)::value;
@@ -406,7 +404,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
     for (int i = 0; i < LIVE; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = v16f{};
-    if constexpr (!ROW) P[1] = v16f{};
+    if constexpr (!ROW && LIVE > 0) {   // the first region's carried promotion adds 0 * 0
+      P[1] = v16f{};
+      sc[LIVE - 1] = 0.f;
+    }
     for (int r = 0; r < G; ++r) {
       // This wave's loads of the region; those of the S - 2 regions after it may be in flight.  (The
       // last tile's stores are waited for too: letting them run behind the first region, by

@@ -304,6 +304,27 @@ def test_gemm_random(scheme, T, k, E, N, K, kind, gather):
     check_gemm(down(c[:int(offsets[-1])]), c64, mag, K, f"{scheme} T={T} {kind}")
 
 
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("T,E,N", [(40, 4, 256), (2000, 3, 512), (1300, 9, 8192)])
+def test_gemm_keeps_a_broken_row_to_itself(scheme, T, E, N):
+    """An infinite scale and NaN codes in one token's row, and in one expert's weight, change no
+    other row: not the tile's neighbours, and not the tiles that follow in a workgroup."""
+    K = 256
+    plan, offsets, _ = _grouped("spread", T, 2, E, T)
+    a = pql.quantize(torch.randn(T, K, device=DEV).bfloat16(), scheme)
+    w = pql.quantize(torch.randn(E * N, K, device=DEV).bfloat16(), scheme, "weight")
+    good = pql.moe_qgemm(a, w, plan, gather=True)
+    rows = torch.zeros(2 * T, dtype=torch.bool, device=DEV)
+    rows[plan.slots.view(T, 2)[17].long()] = True
+    rows[int(offsets[1]):int(offsets[2])] = True           # expert 1
+    a.scales.view(T, -1)[17] = INF
+    a.codes[17, ::3] = 0x7F
+    w.scales.view(E, -1)[1] = INF
+    bad = pql.moe_qgemm(a, w, plan, gather=True)
+    assert torch.equal(bad[~rows], good[~rows])
+    assert not bad[rows].isfinite().any()
+
+
 def test_gemm_follows_no_wild_plan():
     """Offsets and orders outside their ranges stay inside the buffers (and the call ends)."""
     plan, _, _ = _grouped("spread", 20, 2, 4, 1)

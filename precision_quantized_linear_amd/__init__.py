@@ -589,13 +589,13 @@ def _check_vector(t, name: str, dtype, n: int, device) -> None:
         raise ValueError(f"{name} is on {t.device}, the operands on {device}")
 
 
-def _check_plan(plan, device=None) -> None:
+def _check_plan(plan, device, *fields) -> None:
+    """A plan on ``device``, with the sizes of the ``fields`` that the caller hands to the library."""
     if not isinstance(plan, MoePlan):
         raise ValueError("plan must be a MoePlan")
-    device = plan.device if device is None else device
-    _check_vector(plan.offsets, "plan.offsets", torch.int32, plan.n_experts + 1, device)
-    _check_vector(plan.order, "plan.order", torch.int32, plan.tokens * plan.top_k, device)
-    _check_vector(plan.slots, "plan.slots", torch.int32, plan.tokens * plan.top_k, device)
+    for f in fields:
+        n = plan.n_experts + 1 if f == "offsets" else plan.tokens * plan.top_k
+        _check_vector(getattr(plan, f), "plan." + f, torch.int32, n, device)
 
 
 def _check_moe_scheme(scheme: str) -> None:
@@ -679,7 +679,7 @@ def moe_qgemm(a: QTensor, w: QTensor, plan: MoePlan, gather: bool = False,
     has one row per token, which its assignments share; otherwise one row per position."""
     _check_qtensor(a, "a")
     _check_qtensor(w, "w")
-    _check_plan(plan, w.device)
+    _check_plan(plan, w.device, "offsets", "order")
     if a.role != "activation" or w.role != "weight":
         raise ValueError("moe_qgemm takes a quantized activation and a quantized weight")
     if a.scheme != w.scheme:
@@ -720,7 +720,7 @@ def swiglu_quantize(x: torch.Tensor, scheme: str, plan: MoePlan | None = None, o
     if x.shape[1] != 2 * cols:
         raise ValueError("expected gate and up halves of equal width")
     if plan is not None:
-        _check_plan(plan, x.device)
+        _check_plan(plan, x.device, "offsets")
         if rows != plan.tokens * plan.top_k:
             raise ValueError(f"expected the plan's {plan.tokens * plan.top_k} rows, got {rows}")
     if out is not None:
@@ -731,7 +731,10 @@ def swiglu_quantize(x: torch.Tensor, scheme: str, plan: MoePlan | None = None, o
             raise ValueError(f"out is on {out.device}, x on {x.device}")
         q = out
     else:
-        q = _alloc_q(scheme, "activation", rows, cols, x.device)
+        # as _alloc_q lays them out; a width that does not divide is the library's to refuse
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows,) if scheme == "fp8_row" else (rows, cols // 128), dtype=torch.float32, device=x.device)
+        q = QTensor(scheme, "activation", rows, cols, codes, scales)
     _call(lib().pql_swiglu_quantize, "swiglu_quantize", x.device, SCHEMES[scheme], x.data_ptr(), rows, cols,
           x.stride(0) if rows > 1 else 2 * cols, None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_experts,
           q.codes.data_ptr(), q.scales.data_ptr())
@@ -742,8 +745,9 @@ def moe_combine(y: torch.Tensor, plan: MoePlan, weights: torch.Tensor, add: torc
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """Back to tokens: out[t] = add[t] + sum_j weights[t, j] * y[slot of (t, j)], bf16 [T, N],
     summed in fp32.  ``add`` (a shared expert's output, a residual) may be ``out`` itself."""
-    _check_plan(plan)
-    T, P, device = plan.tokens, plan.tokens * plan.top_k, plan.device
+    _check_plan(plan, None)
+    T, P, device = plan.tokens, plan.tokens * plan.top_k, plan.slots.device
+    _check_plan(plan, device, "slots")
     if not isinstance(y, torch.Tensor) or y.dim() != 2:
         raise ValueError("y must be a 2-D tensor")
     N = y.shape[1]

@@ -629,8 +629,9 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
         _check_vector(bias, "bias", torch.float32, E, device)
     _on_device(device)
     k = int(top_k)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=device)
-    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=device)
+    room = min(max(k, 0), E)   # a k outside 1 .. E is the library's to refuse, not the allocator's
+    ids = torch.empty((T, room), dtype=torch.int32, device=device)
+    weights = torch.empty((T, room), dtype=torch.float32, device=device)
     ld = logits.stride(0) if T > 1 else E
     _call(lib().pql_moe_route, "moe_route", device, MOE_SCORES[score], _LOGIT_TYPES[logits.dtype], logits.data_ptr(), T,
           E, ld, _ptr(bias), k, n_groups, top_groups, MOE_GROUP_SCORES[group_score], bool(renormalize), scale,

@@ -167,6 +167,16 @@ def test_route_masked_and_broken_rows(score, biased, groups):
                 top_groups=max(1, groups - 1), group_score="top2")
 
 
+@pytest.mark.parametrize("k", [0, -1, 9, 33, 1 << 40])
+def test_route_refuses_a_k_outside_the_experts_before_any_allocation(k):
+    logits = torch.zeros(4096, 8, device=DEV)
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(ValueError, match="k "):
+        pql.moe_route(logits, k)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 30
+
+
 def test_route_strided_rows_and_unaligned_start():
     buf = torch.randn(40, 131, device=DEV).bfloat16()
     check_route(buf[:, 3:67], 5)

@@ -5,8 +5,8 @@
 // (gather) or p itself.  FP8_BLOCK128: partial products of each 128-wide K-group promoted with
 // s_a[row, g] s_w[e, n / 128, g] in fp32; FP8_ROW: one fp32 sum scaled by s_a[row] s_w[e, n].
 //
-// k_moe_stream: a workgroup owns 32 columns of one expert and walks the expert's rows up to 64 at
-// a time; the weight is streamed past them, as in the few-token qlinear kernels: 8 waves take the
+// k_moe_stream: a workgroup owns 32 columns of one expert and walks the expert's rows (or every
+// z-th pass over them) up to 64 at a time; the weight is streamed past them, as in the few-token qlinear kernels: 8 waves take the
 // K-chunks (128 bytes) round-robin, feed 16x16x128 MFMAs straight from registers, and add
 // their sums in LDS.  Bound by the weight stream.  With fewer assignments than experts the grid has one row of
 // workgroups per assignment, and a workgroup finds the experts that have any by ballots over
@@ -151,25 +151,17 @@ __global__ __launch_bounds__(kThreads, EU) void k_moe_stream(MoeGemmArgs g) {
       }
     }
   };
-  for (int m0 = lo; m0 < hi;) {
-    if (m0 != lo) __syncthreads();
-    const int left = hi - m0;
+  constexpr int kStep = MAXB >= 4 ? 64 : 16;   // rows of a pass; the grid's z splits an expert's passes
+  for (int m0 = lo + kStep * blockIdx.z; m0 < hi; m0 += kStep * gridDim.z) {
+    if (m0 != lo + kStep * (int)blockIdx.z) __syncthreads();   // the last pass's sums are read
     if constexpr (MAXB >= 4) {
-      if (left > 32) {
-        pass(std::integral_constant<int, 4>{}, m0);
-        m0 += 64;
-        continue;
-      }
+      const int left = hi - m0;
+      if (left > 32) pass(std::integral_constant<int, 4>{}, m0);
+      else if (left > 16) pass(std::integral_constant<int, 2>{}, m0);
+      else pass(std::integral_constant<int, 1>{}, m0);
+    } else {
+      pass(std::integral_constant<int, 1>{}, m0);
     }
-    if constexpr (MAXB >= 4) {
-      if (left > 16) {
-        pass(std::integral_constant<int, 2>{}, m0);
-        m0 += 32;
-        continue;
-      }
-    }
-    pass(std::integral_constant<int, 1>{}, m0);
-    m0 += 16;
   }
 }
 
@@ -177,18 +169,23 @@ __global__ __launch_bounds__(kThreads, EU) void k_moe_stream(MoeGemmArgs g) {
 
 // Which kernel, from the sizes alone (the groups' sizes stay on the device): rows per tile, or
 // minus the row blocks of a streaming pass.  Times in us with block-128 scales, evenly routed:
-//   rows per expert          2      4      8     16     32     64    128
+//   rows per expert          2      4      8     16     32     64    128    256
 //   E = 64, N = 4096, K = 2048 (1024 tiles and more)
 //     stream, 1 block       62     76    106    154    256
 //     tiles of 128          77     97    100    104    114
 //   E = 16, N = 2816, K = 2048 (176 tiles)
-//     stream, 1 / 4 blocks  17     --     21     31     43     69    120
-//     tiles of 128          20     --     26     26     27     30     37
-//   E = 8, N = 1024, K = 1024 (32 tiles)
-//     stream, 1 / 4 blocks 4.2    4.3    4.8    5.6    7.5   11.5   20.8
-//     tiles of 128          11     11     11     11     13     16     17
+//     stream, 1 / 4 blocks  17     --     21     31     43     71    122
+//     tiles of 128          20     --     26     26     27     29     50
+//   E = 8, N = 1024, K = 2048 (32 tiles)
+//     stream, 4 blocks                            9     13     19     28     44
+//     tiles of 128                               17     21     24     25     26
+//   E = 4, N = 4096, K = 2048 (64 tiles)
+//     stream, 4 blocks                           13     17     26     42     78
+//     tiles of 128                               17     20     23     26     27
 // A tile reads a weight once for 128 rows; the stream reads it once per pass (16 or 64 rows), but
-// spreads an expert over N / 32 workgroups, so it holds on longer where tiles leave CUs idle.
+// spreads an expert over N / 32 workgroups and more, so it holds on longer where tiles leave CUs
+// idle: up to 2^19 outputs at 32 rows per expert and more, whatever K (512, 2048 and 8192
+// measured: within 5 % of the better there), and below 2048 rows over tiles.
 // Tiles of 256 rows read the weight half as often and win where both shapes fill the chip (65536
 // rows, 64 experts, N = 4096, K = 2048: 714 against 807; 16 experts of 128 rows, N = 2816: 41 against 37).
 static int kernel_choice(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t N, int64_t K) {
@@ -196,13 +193,19 @@ static int kernel_choice(int64_t P, int64_t E, bool gather, int64_t a_rows, int6
   const int64_t tiles = (P / 128 + active) * tiles_n;
   if (per < 6) return -1;
   // gathered rows of a tile are addressed with 32-bit offsets from the activation's start
-  if (per < 2048 / tiles || (gather && a_rows * K > int64_t(0xFFFF0000))) return per <= 8 ? -1 : -4;
+  const bool few = per < 2048 / tiles || (per >= 32 && P * N <= (1 << 19));
+  if (few || (gather && a_rows * K > int64_t(0xFFFF0000))) return per <= 8 ? -1 : -4;
   return per >= 32 && (P / 256 + active) * tiles_n >= 512 ? 256 : 128;
 }
 
 template <bool ROW>
 static hipError_t launch_stream(int blocks, const MoeGemmArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.N + kCols - 1) / kCols), (unsigned)std::min(g.E, g.P));
+  // The passes of an expert (of twice the mean rows) are split over up to 1024 workgroups in all: 4
+  // experts of 128 rows, N = 128, K = 2048 take 9.8 us, not split 24.5; 8 of 64 rows, N = 512, 10.9
+  // and 17.1.  512 are too few (16 experts of 64 rows, N = 1024: 32 against 25), 2048 no better.
+  const int64_t cols = (g.N + kCols - 1) / kCols, slots = std::min(g.E, g.P), passes = 2 * (g.P / slots) / 64;
+  const int64_t split = std::max<int64_t>(1, std::min(passes, 1024 / (cols * slots)));
+  const dim3 grid((unsigned)cols, (unsigned)slots, (unsigned)split);
   if (blocks == 1) hipLaunchKernelGGL((k_moe_stream<ROW, 1, 6>), grid, dim3(kThreads), 0, st, g);
   else hipLaunchKernelGGL((k_moe_stream<ROW, 4, 3>), grid, dim3(kThreads), 0, st, g);
   return hipGetLastError();

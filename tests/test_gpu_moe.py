@@ -239,6 +239,12 @@ GEMM_CASES = [
     ("fp8_row", 37, 3, 10, 520, 384, "spread"), ("fp8_row", 40, 2, 3, 264, 512, "dropped"),
     ("fp8_row", 300, 2, 5, 33, 256, "crowded"), ("fp8_row", 700, 1, 2, 577, 384, "spread"),
     ("fp8_row", 290, 2, 4, 256, 128, "one"), ("fp8_row", 1100, 3, 4, 712, 512, "spread"),
+    # tiles of 128 rows and columns past the last whole one
+    ("fp8_block128", 300, 2, 5, 1408, 256, "crowded"), ("fp8_block128", 290, 2, 4, 1280, 128, "one"),
+    ("fp8_row", 300, 2, 5, 1401, 256, "crowded"), ("fp8_row", 700, 1, 2, 1601, 384, "spread"),
+    ("fp8_row", 500, 2, 4, 1032, 640, "dropped"),
+    # passes of the stream split over workgroups, more of them than the mean asks for
+    ("fp8_block128", 900, 1, 3, 128, 256, "crowded"), ("fp8_row", 1500, 2, 8, 100, 384, "one"),
     # the 256-row tiles: experts of a few rows to several tiles, columns past the last whole tile
     ("fp8_block128", 1430, 3, 130, 1024, 384, "spread"), ("fp8_block128", 1350, 2, 9, 8064, 256, "crowded"),
     ("fp8_row", 1430, 3, 130, 1000, 384, "dropped"), ("fp8_row", 1350, 2, 9, 8190, 256, "crowded"),
@@ -312,6 +318,54 @@ def test_gemm_random(scheme, T, k, E, N, K, kind, gather):
     c = pql.moe_qgemm(pql.quantize(up(x), scheme), pql.quantize(up(wt), scheme, "weight"), plan, gather=gather)
     c64, mag = moe.gemm(a, w, offsets, order, k, gather)
     check_gemm(down(c[:int(offsets[-1])]), c64, mag, K, f"{scheme} T={T} {kind}")
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("what,T,k,E,N,K,gather", [
+    ("gathered activation", (1 << 20) + 5, 1, 2, 128, 4224, True), ("activation", (1 << 20) + 5, 1, 2, 128, 4224, False),
+    ("result", (1 << 20) + 5, 1, 2, 4352, 128, False), ("weights", 300, 2, 130, 8192, 4352, True)])
+def test_gemm_past_32_bit_offsets(scheme, what, T, k, E, N, K, gather):
+    """Operands and results of more than 2^32 bytes: sampled rows, the first and last among them.
+
+    The codes are uniform over all magnitudes, which check_gemm's accumulation term (8 K 2^-24 T) is
+    not made for: the fp8 matrix instruction first sums groups of 8 products, cut at 2^-13 of the
+    group's largest 2^(exponent of a + exponent of w) (measured: beside two cancelling 2^8 x 2^8,
+    six products of 4 are lost, of 8 kept, of 12 count as 8).  The largest is exact, so a group
+    loses at most 7 2^-13 of its largest product, all of them 7 2^-13 T: with
+    T' = T (1 + 7 2^-13 / (8 K 2^-24)) = T (1 + 1792 / K) the term covers both."""
+    g = torch.Generator(device=DEV).manual_seed(T + N)
+    block = scheme == "fp8_block128"
+
+    def operand(role, rows, scale_shape):
+        codes = torch.randint(0, 127, (rows, K), dtype=torch.uint8, device=DEV, generator=g)   # no NaN codes
+        if role == "weight":
+            codes[:, ::3] += 128
+        scales = torch.rand(scale_shape, device=DEV, generator=g) + 0.5
+        return pql.QTensor(scheme, role, rows, K, codes, scales)
+
+    rows = T if gather else T * k
+    a = operand("activation", rows, (rows, K // 128) if block else (rows,))
+    w = operand("weight", E * N, (E * N // 128, K // 128) if block else (E * N,))
+    assert max(a.codes.numel(), w.codes.numel(), 2 * T * k * N) > 1 << 32
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device=DEV, generator=g)
+    plan = pql.moe_plan(ids, E)
+    c = pql.moe_qgemm(a, w, plan, gather=gather)
+    table = dev(F.e4m3_decode(np.arange(256, dtype=np.uint8)).astype(np.float64))
+    offsets, P = plan.offsets.cpu().numpy(), T * k
+    at = np.unique(np.concatenate([[0, 1, P - 2, P - 1], np.random.default_rng(1).integers(0, P, 40),
+                                   [x for o in offsets for x in (o - 1, o) if 0 <= x < P]]))
+    for e in range(E):
+        p = at[(at >= offsets[e]) & (at < offsets[e + 1])]
+        if e % 16 and e != E - 1 and E > 16 or not len(p):
+            continue
+        p = torch.as_tensor(p, device=DEV)
+        r = plan.order[p].long() // k if gather else p
+        A = table[a.codes[r].long()] * (a.scales[r].double().repeat_interleave(128, 1) if block else a.scales[r].double()[:, None])
+        ws = w.scales[e * (N // 128):(e + 1) * (N // 128)].double().repeat_interleave(128, 0).repeat_interleave(128, 1) \
+            if block else w.scales[e * N:(e + 1) * N].double()[:, None]
+        W = table[w.codes[e * N:(e + 1) * N].long()] * ws
+        mag = (A.abs() @ W.abs().t()).cpu().numpy()
+        check_gemm(down(c[p]), (A @ W.t()).cpu().numpy(), mag, K, f"{what} {scheme}", t_acc=mag * (1 + 1792 / K))
 
 
 @pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kThreads, EU) void k_moe_stream(MoeGemmArgs g) {
 // A tile reads a weight once for 128 rows; the stream reads it once per pass (16 or 64 rows), but
 // spreads an expert over N / 32 workgroups and more, so it holds on longer where tiles leave CUs
 // idle: up to 2^19 outputs at 32 rows per expert and more, whatever K (512, 2048 and 8192
-// measured: within 5 % of the better there), and below 2048 rows over tiles.
+// measured: at worst 9 % over the better there), and below 2048 rows over tiles.
 // Tiles of 256 rows read the weight half as often and win where both shapes fill the chip (65536
 // rows, 64 experts, N = 4096, K = 2048: 714 against 807; 16 experts of 128 rows, N = 2816: 41 against 37).
 static int kernel_choice(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t N, int64_t K) {

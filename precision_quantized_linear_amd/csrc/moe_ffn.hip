@@ -13,8 +13,12 @@ namespace {
 
 // ---------------------------------------------------------------- swiglu + quantize
 // h = g / (1 + exp(-g)) * u in fp32 from a row's bf16 gate and up halves, then the scheme's
-// activation rule on h (never rounded to bf16 in between).  exp(-g) is 2^(-g log2 e); it
-// overflows to infinity below g = -88, where the quotient is the limit, -0.
+// activation rule on h (never rounded to bf16 in between).  exp(-g) is 2^(-g log2 e).  Far below
+// zero 1 + exp(-g) nears the end of fp32 (its reciprocal is subnormal from g = -87.3 on, which the
+// instruction flushes, and it overflows at -88.7), but a large u brings h back well inside:
+// silu(-90) 1e6 = -7e-32, silu(-190) 3e38 = -2e-42.  There 1 + exp(-g) is exp(-g) to all 24
+// bits, and h = g 2^(g log2 e) u takes its power of two last, in one rounding.  A chunk without such
+// a gate pays for their minimum alone.
 //
 // Bound by memory (4 bytes read, 1 written per element): 65536 rows of F = 2048 with block
 // scales take 125 us, 5.4 TB/s; 222 rows of 1408 with row scales 3 us.  A lane holds 8 columns
@@ -24,12 +28,29 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
+constexpr float kFarGate = -80.0f;
+// For g < kFarGate.  2^-10 keeps the product with u finite; gates below -300 give 0 for any finite u.
+__device__ __forceinline__ float far_silu_mul(float g, float u) {
+  g = fmaxf(g, -300.0f);
+  const float y = g * 1.44269504f, n = __builtin_rintf(y);
+  return ldexpf(__builtin_amdgcn_exp2f(y - n) * 0x1p-10f * g * u, (int)n + 10);
+}
+
 __device__ __forceinline__ void swiglu_chunk(uint4 gc, uint4 uc, float (&h)[8]) {
   float g[8], u[8];
   chunk_to_f32(gc, g);
   chunk_to_f32(uc, u);
+  float least = g[0];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = silu_mul(g[j], u[j]);
+  for (int j = 0; j < 8; ++j) {
+    h[j] = silu_mul(g[j], u[j]);
+    least = fminf(least, g[j]);
+  }
+  if (least < kFarGate) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (g[j] < kFarGate) h[j] = far_silu_mul(g[j], u[j]);
+  }
 }
 
 __device__ __forceinline__ float absmax8(const float (&h)[8]) {

@@ -66,3 +66,20 @@ def test_swiglu_far_gates(scheme, cols):
     check_swiglu_everywhere(x, scheme, q)
     assert (q.scales.reshape(rows, -1)[18] == 1).all() and not (q.codes[18] & 0x7F).any()
     assert (q.scales.reshape(rows, -1)[20] < 1e-33).all() and ((q.codes[20] & 0x7F) == 0x7E).all()
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("cols", [128, 384, 2176, 8320])
+def test_swiglu_subnormal_scales(scheme, cols):
+    """Largest |h| of n 2^-149: the scale is n / 448 rounded to whole steps of 2^-149, so a quotient
+    reaches n, well past 448 (n = 656: scale 1 step, quotient 656): the code saturates there, as every
+    cast does."""
+    rng = np.random.default_rng(cols)
+    tops = np.array([1, 200, 224, 228, 300, 448, 480, 600, 656, 672, 1000, 1120, 1360, 2000, 5000, 20000])
+    g = np.full((len(tops), cols), 2.0 ** -70)               # silu(g) = 2^-71 exactly, to fp32
+    n = tops[:, None] * rng.uniform(-1.0, 1.0, (len(tops), cols))
+    n[:, ::128] = tops[:, None]
+    x = F.f32_to_bf16_rne(np.concatenate([g, n * 2.0 ** -78], axis=1).astype(np.float32))
+    q = pql.swiglu_quantize(up(x), scheme)
+    check_swiglu_everywhere(x, scheme, q)
+    assert ((q.codes & 0x7F) != 0x7F).all()

@@ -818,6 +818,18 @@ pql_status check_moe_scheme(int scheme) {
   return PQL_OK;
 }
 
+// The sizes of a grouped product: T k rows, E weights [N, K].
+pql_status check_moe_gemm_shape(int scheme, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+  pql_status st = check_moe_scheme(scheme);
+  if (st != PQL_OK) return st;
+  if ((st = check_assignments(T, k, E)) != PQL_OK) return st;
+  if ((st = check_gemm_shape(scheme, T * k, N, K)) != PQL_OK) return st;
+  if (N > (int64_t(1) << 20)) return fail(PQL_ERR_INVALID_ARGUMENT, "N above 2^20 is not supported");
+  if (E * N > (kMaxSpan / K)) return fail(PQL_ERR_INVALID_ARGUMENT, "an E x N x K weight of %lld x %lld x %lld is too large",
+                                          (long long)E, (long long)N, (long long)K);
+  return PQL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -923,14 +935,9 @@ static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales
                                  const void* w_codes, const void* w_scales, const int32_t* offsets,
                                  const int32_t* order, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K, void* c,
                                  int64_t ldc, void* stream) {
-  pql_status st = check_moe_scheme(scheme);
+  pql_status st = check_moe_gemm_shape(scheme, T, k, E, N, K);
   if (st != PQL_OK) return st;
-  if ((st = check_assignments(T, k, E)) != PQL_OK) return st;
   const int64_t P = T * k;
-  if ((st = check_gemm_shape(scheme, P, N, K)) != PQL_OK) return st;
-  if (N > (int64_t(1) << 20)) return fail(PQL_ERR_INVALID_ARGUMENT, "N above 2^20 is not supported");
-  if (E * N > (kMaxSpan / K)) return fail(PQL_ERR_INVALID_ARGUMENT, "an E x N x K weight of %lld x %lld x %lld is too large",
-                                          (long long)E, (long long)N, (long long)K);
   if ((st = check_ld("ldc", ldc, P, N, false)) != PQL_OK) return st;
   const int64_t want = gather ? T : P;
   if (a_rows != want)
@@ -966,11 +973,13 @@ static pql_status moe_qgemm_impl(int scheme, const void* a, const void* a_scales
 }
 
 const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
-  if ((scheme != PQL_FP8_ROW && scheme != PQL_FP8_BLOCK128) || T < 1 || T > pql::kMoeMaxRows || k < 1 ||
-      k > pql::kMoeMaxTopK || E < 1 || E > pql::kMoeMaxExperts || N < 1 || N > (int64_t(1) << 20) || K < 1 ||
-      K > (int64_t(1) << 20))
-    return "";
-  return pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, gather != 0, T, k, E, N, K);
+  std::string text;   // the checks' own error text is not this call's
+  text.swap(g_error);
+  // rows of the narrowest result, ldc = N, span P N elements
+  const bool valid = check_moe_gemm_shape(scheme, T, k, E, N, K) == PQL_OK && T > 0 &&
+                     check_ld("ldc", N, T * k, N, false) == PQL_OK;
+  text.swap(g_error);
+  return valid ? pql::moe_gemm_kernel_name(scheme == PQL_FP8_ROW, gather != 0, T, k, E, N, K) : "";
 }
 
 pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_t a_rows, int gather,

@@ -200,3 +200,25 @@ def test_rejected_calls_are_logged():
     assert lines == ["[pql] moe_plan T=4 k=2 E=0: rejected (status 1): E must be 1 .. 1024 (got 0)",
                      "[pql] moe_qgemm MXFP8 T=4 k=2 E=8 N=256 K=256: rejected (status 2): "
                      "defined for FP8_ROW and FP8_BLOCK128 only (got MXFP8)"]
+
+
+@pytest.mark.parametrize("scheme,T,k,E,N,K", [
+    ("fp8_block128", 4, 2, 8, 200, 256), ("fp8_row", 4, 2, 8, 256, 100), ("fp8_block128", 4, 2, 8, 256, 200),
+    ("fp8_row", 1 << 23, 2, 8, 256, 256), ("fp8_block128", (1 << 24) - 1, 32, 8, 256, 256), ("fp8_row", 1 << 24, 1, 8, 256, 256),
+    ("fp8_row", 4, 2, 1024, 1 << 20, 1 << 20), ("fp8_row", 4, 2, 8, 1 << 20, 1 << 18), ("fp8_row", 4, 2, 8, (1 << 20) + 1, 256),
+    ("fp8_row", (1 << 24) - 1, 1, 8, 1 << 17, 256), ("fp8_row", 4, 33, 64, 256, 256), ("fp8_row", 4, 2, 1025, 256, 256), ("fp8_row", -1, 2, 8, 256, 256),
+    ("fp8_row", 4, 2, 8, 256, 1 << 21), ("fp8_row", 4, 0, 8, 256, 256), ("fp8_row", 4, 2, 0, 256, 256), ("int8_row", 4, 2, 8, 256, 256)])
+@pytest.mark.parametrize("gather", [0, 1])
+def test_no_kernel_is_named_for_a_refused_product(scheme, T, k, E, N, K, gather):
+    """Every shape that pql_moe_qgemm refuses has the name "", and asking leaves the error text alone."""
+    rows = T if gather else T * k
+    assert _gemm(pql.SCHEMES[scheme], rows=rows, gather=gather, T=T, k=k, E=E, N=N, K=K, ldc=N) in (INVALID, UNSUPPORTED)
+    before = pql.lib().pql_last_error()
+    assert pql.moe_kernel_name(scheme, T, k, E, N, K, gather) == ""
+    assert pql.lib().pql_last_error() == before
+
+
+@pytest.mark.parametrize("scheme,N", [("fp8_block128", 256), ("fp8_row", 200), ("fp8_row", 1)])
+def test_kernels_are_named_for_accepted_products(scheme, N):
+    for T, k in ((1, 1), (37, 6), ((1 << 24) - 1, 1), ((1 << 19) - 1, 32)):
+        assert pql.moe_kernel_name(scheme, T, k, 64, N, 512).startswith("k_moe_")

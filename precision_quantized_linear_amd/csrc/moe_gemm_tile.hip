@@ -77,23 +77,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
   // ---- row tiles before each expert: prefix[e], prefix[E] = all of them
   int* const prefix = reinterpret_cast<int*>(smem + S::kPrefix);
   if (wave == 0) {
+    const int most = most_row_tiles<S::BM>(g);
     int carry = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
       const int e = e0 + lane;
-      int lo = 0, hi = 0;
-      if (e < g.E) expert_range(g, e, lo, hi);
-      const int n = (hi - lo + S::BM - 1) / S::BM;
+      const int n = e < g.E ? row_tiles_of<S::BM>(g, e) : 0;
       int s = n;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int u = __shfl_up(s, o);
         if (lane >= o) s += u;
       }
-      if (e < g.E) prefix[e] = carry + s - n;
+      if (e < g.E) prefix[e] = std::min(carry + s - n, most);
       carry += __shfl(s, 63);
     }
-    // a plan has at most P / BM + E row tiles; wild offsets are cut there
-    if (lane == 0) prefix[g.E] = std::min(carry, g.P / S::BM + g.E);
+    if (lane == 0) prefix[g.E] = std::min(carry, most);
   }
   __syncthreads();
   const int row_tiles = __builtin_amdgcn_readfirstlane(prefix[g.E]);
@@ -114,23 +112,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_moe_tile(MoeGemmArgs g) {
     if (wave != 0) return;
     const int el = fresh_lane();
     const int L = sched.first + std::min(base + el, my_tiles - 1) * sched.stride;
-    int e = 0, above = g.E;   // prefix[e] * tiles_n <= L < prefix[above] * tiles_n
-    while (above - e > 1) {
-      const int mid = (e + above) >> 1;
-      if (prefix[mid] * tiles_n <= L) e = mid;
-      else above = mid;
-    }
-    int lo, hi;
-    expert_range(g, e, lo, hi);
-    const int tiles_m = (hi - lo + S::BM - 1) / S::BM;
-    const int l = L - prefix[e] * tiles_n;
-    constexpr int kGroupM = 4;
-    const int group = l / (kGroupM * tiles_n);
-    const int gm = std::max(1, std::min(tiles_m - group * kGroupM, kGroupM));
-    const int r = l - group * kGroupM * tiles_n;
-    const int m0 = lo + (group * kGroupM + r % gm) * S::BM;
-    tiles[2 * el] = m0;
-    tiles[2 * el + 1] = (e * 4096 + r / gm) * 512 + std::max(0, std::min(S::BM, hi - m0));
+    const TilePlace at = tile_place<S::BM>(g, prefix, tiles_n, L);
+    tiles[2 * el] = at.m0;
+    tiles[2 * el + 1] = (at.e * 4096 + at.column) * 512 + at.rows;
   };
   auto tile_at = [&](int k) __attribute__((always_inline)) {
     const int i = 2 * ((k - tile_base) & 63);

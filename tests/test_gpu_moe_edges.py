@@ -4,9 +4,10 @@ import pytest
 import torch
 
 import precision_quantized_linear_amd as pql
+from gemm_check import check_gemm_exact, exact_operand
 from oracle import formats as F
 from oracle import moe
-from test_gpu_moe import up
+from test_gpu_moe import down, up
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +84,93 @@ def test_swiglu_subnormal_scales(scheme, cols):
     q = pql.swiglu_quantize(up(x), scheme)
     check_swiglu_everywhere(x, scheme, q)
     assert ((q.codes & 0x7F) != 0x7F).all()
+
+
+# ---------------------------------------------------------------- grouped products
+KERNELS = [   # a shape for each kernel
+    ("fp8_row", "stream<1", 5, 2, 64, 200, 256), ("fp8_block128", "stream<1", 5, 2, 64, 256, 256),
+    ("fp8_row", "stream<1", 40, 3, 30, 200, 256), ("fp8_block128", "stream<1", 40, 3, 30, 256, 256),
+    ("fp8_row", "stream<4", 20, 2, 4, 264, 384), ("fp8_block128", "stream<4", 20, 2, 4, 256, 384),
+    ("fp8_row", "tile<128", 300, 2, 5, 1401, 256), ("fp8_block128", "tile<128", 300, 2, 5, 1408, 256),
+    ("fp8_row", "tile<256", 1350, 2, 9, 8190, 256), ("fp8_block128", "tile<256", 1350, 2, 9, 8064, 256),
+]
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("scheme,kernel,T,k,E,N,K", KERNELS)
+def test_no_kernel_follows_a_wild_plan(scheme, kernel, T, k, E, N, K, gather):
+    """Offsets and orders of any value: the call ends and writes nothing outside the result."""
+    assert pql.moe_kernel_name(scheme, T, k, E, N, K, gather) == f"k_moe_{kernel}, {scheme}>"
+    rng = np.random.default_rng(N)
+    a = pql.quantize(torch.randn(T if gather else T * k, K, device=DEV).bfloat16(), scheme)
+    w = pql.quantize(torch.randn(E * N, K, device=DEV).bfloat16(), scheme, "weight")
+    plan = pql.moe_plan(torch.zeros(T, k, dtype=torch.int32, device=DEV), E)
+    big = np.iinfo(np.int32)
+    overlapping = np.where(np.arange(E + 1) % 2, big.max, big.min)
+    for offsets in (rng.integers(big.min, big.max, E + 1), rng.integers(-5, T * k + 5, E + 1), overlapping,
+                    np.full(E + 1, big.max), np.full(E + 1, big.min), np.arange(E + 1)[::-1] * 7):
+        plan.offsets.copy_(torch.from_numpy(offsets.astype(np.int32)))
+        plan.order.copy_(torch.from_numpy(rng.integers(big.min, big.max, T * k).astype(np.int32)))
+        wide = torch.full((T * k + 300, N + 6), 7.0, device=DEV).bfloat16()
+        pql.moe_qgemm(a, w, plan, gather=gather, out=wide[:T * k, 3:3 + N])
+        wide[:T * k, 3:3 + N] = 7.0
+        assert (wide == 7.0).all()
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("kernel,T,E,N,K", [("tile<256", (1 << 20) - 20, 2, 1024, 4096), ("tile<128", 65535, 2, 256, 65536),
+                                            ("stream<4", 65536, 2, 256, 65536)])
+def test_gathered_activation_at_the_32_bit_border(scheme, kernel, T, E, N, K):
+    """Tiles gather by 32-bit offsets up to an activation of 2^32 - 2^16 bytes; one row more and the
+    stream takes it.  Codes of 0, +-1 and +-2 and scales of 1, 2 and 4: every sum is a whole number
+    below 2^24, exact in any order, so sampled rows must equal their rounding to bf16."""
+    assert pql.moe_kernel_name(scheme, T, 1, E, N, K, True) == f"k_moe_{kernel}, {scheme}>"
+    g = torch.Generator(device=DEV).manual_seed(K)
+    block = scheme == "fp8_block128"
+    table = torch.zeros(64, dtype=torch.uint8, device=DEV)
+    table[:4] = torch.tensor([0x38, 0x40, 0xB8, 0xC0], dtype=torch.uint8, device=DEV)   # 1, 2, -1, -2
+
+    def operand(role, rows):
+        codes = torch.empty(rows, K, dtype=torch.uint8, device=DEV)
+        for r in range(0, rows, 4096):
+            part = codes[r:r + 4096]
+            part.copy_(table[torch.randint(0, 64, part.shape, device=DEV, generator=g)])
+        shape = (rows,) if not block else (rows, K // 128) if role == "activation" else (rows // 128, K // 128)
+        return pql.QTensor(scheme, role, rows, K, codes, 2.0 ** torch.randint(0, 3, shape, device=DEV, generator=g).float())
+
+    a, w = operand("activation", T), operand("weight", E * N)
+    ids = torch.randint(0, E, (T, 1), dtype=torch.int32, device=DEV, generator=g)
+    plan = pql.moe_plan(ids, E)
+    c = pql.moe_qgemm(a, w, plan, gather=True)
+    value = torch.from_numpy(F.e4m3_decode(np.arange(256, dtype=np.uint8))).to(DEV)
+    offsets = plan.offsets.tolist()
+    for e in range(E):
+        lo, hi = offsets[e], offsets[e + 1]
+        p = torch.cat([torch.tensor([lo, lo + 1, hi - 2, hi - 1], device=DEV),
+                       torch.randint(lo, hi, (24,), device=DEV, generator=g)])
+        r = plan.order[p].long()
+        s = a.scales[r].double()
+        A = value[a.codes[r].long()] * (s.repeat_interleave(128, 1) if block else s[:, None])
+        mine = slice(e * N, (e + 1) * N)
+        s = w.scales[mine].double()[:, None] if not block else \
+            w.scales[e * (N // 128):(e + 1) * (N // 128)].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+        want = A @ (value[w.codes[mine].long()] * s).t()
+        assert want.abs().max() < 1 << 24
+        assert torch.equal(c[p], want.float().bfloat16())
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+def test_a_crowded_expert_in_the_stream(scheme):
+    """Every token's first choice is one expert of 256, the second is spread: the streaming kernel walks
+    the crowded expert's 512 rows in passes of 16 beside experts of a few rows and empty ones."""
+    T, k, E, N, K = 512, 2, 256, 256, 256
+    rng = np.random.default_rng(3)
+    ids = np.stack([np.full(T, 200), rng.integers(0, 150, T)], axis=1)
+    assert pql.moe_kernel_name(scheme, T, k, E, N, K, True) == f"k_moe_stream<1, {scheme}>"
+    plan = pql.moe_plan(torch.from_numpy(ids.astype(np.int32)).to(DEV), E)
+    offsets, order = plan.offsets.cpu().numpy(), plan.order.cpu().numpy()
+    assert offsets[201] - offsets[200] == T
+    a, w = exact_operand(scheme, "activation", T, K, 1), exact_operand(scheme, "weight", E * N, K, 2)
+    c = pql.moe_qgemm(pql.from_numpy(a, DEV), pql.from_numpy(w, DEV), plan, gather=True)
+    c64, _ = moe.gemm(a, w, offsets, order, k, True)
+    check_gemm_exact(down(c), c64, f"crowded {scheme}")

@@ -255,14 +255,20 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(RouteArgs r) {
   };
 
   // ---- fp32 keys, and the bound of their error, in units of u = 2^-24 (half an ulp of 1).  In
-  // rough() the exponential of an argument y is off by (1.5 |y| + 2) u relative: y log2 e is
-  // rounded, as is log2 e, and the instruction is within one ulp.
-  //   sigmoid: that enters as s (1 - s) (1.5 |y| + 2) <= 0.9, the sum and the reciprocal of a
+  // rough() the exponential of an argument y is off by (a |y| + 2) u relative: log2 e is rounded
+  // (0.23), its product with y (1) and the softmax's y = x - top (1), and the instruction is within
+  // one ulp (2): a = 1.23 and 2.23.
+  //   sigmoid: that enters as s (1 - s) (1.23 |y| + 2) <= 0.7, the sum and the reciprocal of a
   //   value below 1 add 3: below 4 u.
-  //   softmax: it enters as s (1.5 |y| + 2) <= 2.6; the denominator's relative error, the terms'
-  //   (their mean |y| is below ln E = 7) and at most 22 roundings, is below 35, its reciprocal
-  //   and the product add 3: below 41 u.
-  // Adding the bias rounds once more; 6 and 48, and 2 |c| u, leave room.
+  //   softmax: it enters as s (2.23 |y| + 2) <= 2.1 (s <= exp(y), y <= 0); the denominator's relative
+  //   error, the terms' (their mean |y| is below ln E = 7) and at most 22 roundings, is below 40, its
+  //   reciprocal and the product add 3: below 46 u.
+  // Adding the bias rounds once more, |c| u.  Two choices are told apart by 2 delta, delta = (6 or
+  // 50, and 2 |c|) u: two errors, and |c| u for the rounding of their difference or of c - 2 delta,
+  // 2 (46 + |c|) + |c|.  A group's sum of two choices rounds by 2 |c| u, as does a sum plus or
+  // minus the slack that tells two of them apart: 2 (2 (4 or 46, and |c|) + 2 |c|) + 2 |c| =
+  // 16 or 184, and 10 |c|; 18 and 192 leave room for the slack's own part in the last rounding (it
+  // is below 1: see `unsure`).
   float key[V];
   float biggest = 0.0f;
 #pragma unroll
@@ -282,9 +288,10 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(RouteArgs r) {
   }
   bool unsure = false;
   float delta = 0.0f;
+  biggest = BIASED ? lanes_max<L>(biggest) : 1.0f;   // scores are at most 1
   if constexpr (BIASED) {
-    delta = ((softmax ? 48.0f : 6.0f) + 2.0f * lanes_max<L>(biggest)) * 0x1p-24f;
-    unsure = !(delta < 1.0f) || r.k > L - 2;   // huge biases; no lane left for a further candidate
+    delta = ((softmax ? 50.0f : 6.0f) + 2.0f * biggest) * 0x1p-24f;
+    unsure = !(delta < 0.125f) || r.k > L - 2;   // biases of 2^20 and more; no lane left for a further candidate
   }
   if (r.groups > 1) {
     const bool exact = !BIASED && r.group_score == 0;   // the logits themselves
@@ -298,7 +305,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(RouteArgs r) {
       choice[v * L + lane] = c;
     }
     asm volatile("" ::: "memory");
-    const float slack = exact ? 0.0f : 4.0f * (BIASED ? delta : 50.0f * 0x1p-24f);
+    const float slack = exact ? 0.0f : ((softmax ? 192.0f : 18.0f) + 10.0f * biggest) * 0x1p-24f;
     bool level = false;   // group scores too close for fp32
     uint64_t kept = kept_groups<L, float>(r, per, choice, reinterpret_cast<float*>(group_lds[sub]), lane, slack, level);
     if (__ballot(level)) {   // their choices in fp64, one token at a time on all 64 lanes

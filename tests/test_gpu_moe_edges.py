@@ -174,3 +174,84 @@ def test_a_crowded_expert_in_the_stream(scheme):
     c = pql.moe_qgemm(pql.from_numpy(a, DEV), pql.from_numpy(w, DEV), plan, gather=True)
     c64, _ = moe.gemm(a, w, offsets, order, k, True)
     check_gemm_exact(down(c), c64, f"crowded {scheme}")
+
+
+# ---------------------------------------------------------------- route
+def check_route_rows(x, k, rows, **kw):
+    """The kernel on all of ``x``, the oracle on ``rows``: ids equal, weights within what the kernel's
+    arithmetic allows.  A score s = exp(d) / z of the distance d = x - max is off by |d| (the
+    rounding of d), 2 (the exponential), 40 (z: the terms' 2.23 |d| + 2 with a mean |d| below ln 1024, 22
+    roundings) and 1 (the quotient) units of 2^-24; a sigmoid by less; a weight of renormalized
+    scores by that and the weighted mean of the others', 1 for its own rounding and half a step of
+    the subnormal grid.  Scores below 2^-100 are formed in 64 bits, with no error to speak of."""
+    bias = kw.get("bias")
+    ids, w = pql.moe_route(x, k, **kw)
+    x64 = x[rows].double().cpu().numpy()
+    want_ids, want_w = moe.route(x64, k, **{**kw, "bias": None if bias is None else bias.cpu().numpy()})
+    assert np.array_equal(ids[rows].cpu().numpy(), want_ids)
+    got = w[rows].double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want_w))
+    top = np.where(x64 < np.inf, x64, -np.inf).max(1, keepdims=True)
+    d = np.abs(np.take_along_axis(x64, np.maximum(want_ids, 0), 1) - np.where(top > -np.inf, top, 0.0))
+    d = np.where((want_ids >= 0) & (d < 70.0), d, 0.0) * (kw.get("score", "softmax") == "softmax")
+    if kw.get("renormalize", True):
+        total = np.abs(want_w).sum(1, keepdims=True)
+        d = d + (np.abs(want_w) * d).sum(1, keepdims=True) / np.where(total > 0, total, 1.0) + 43
+    ok = np.abs(got - want_w) <= (d + 44) * 2.0 ** -24 * np.abs(want_w) + 2.0 ** -150
+    assert ok[~np.isnan(want_w)].all(), f"{int((~ok).sum())} weights off"
+
+
+@pytest.mark.parametrize("k", [17, 31, 32])
+@pytest.mark.parametrize("E,n,top", [(64, 4, 3), (128, 8, 4), (250, 10, 5), (512, 8, 3), (1000, 4, 1)])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", True), ("softmax", True)])
+def test_route_more_results_than_lanes(E, n, top, k, score, biased):
+    """Many tokens, so 16 or 32 lanes each, and up to 32 experts per token: a lane of 16 keeps a second
+    result, and with a bias no lane is left for a further candidate."""
+    T = 2061
+    g = torch.Generator().manual_seed(E * k)
+    x = torch.randn(T, E, generator=g).to(DEV)
+    x[7, E // 2:] = -float("inf")
+    x[8, 3:] = -float("inf")                                 # fewer experts than results
+    x[9, 5] = float("nan")
+    bias = (0.1 * torch.randn(E, generator=g)).to(DEV) if biased else None
+    rows = torch.cat([torch.arange(24), torch.randint(0, T, (60,), generator=g), torch.arange(T - 9, T)]).to(DEV)
+    check_route_rows(x, k, rows, score=score, bias=bias)
+    check_route_rows(x, k, rows, score=score, bias=bias, n_groups=n, top_groups=top, renormalize=False, scale=2.5)
+
+
+@pytest.mark.parametrize("T", [40, 2100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_weights_beside_the_lowest_value(T, score, biased):
+    """Masks of the type's lowest value, and logits far from the row's largest."""
+    E, k = 48, 12
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, E, generator=g)
+    low = torch.finfo(torch.float32).min
+    x[0::8, ::2] = low
+    x[1::8, 6:] = low                                        # fewer real logits than results
+    x[2::8] = low
+    x[3::8] *= 30.0
+    x[4::8] *= 1000.0
+    x[5::8, 1:] = -float("inf")
+    x[6::8] *= 1e-30
+    bias = (0.1 * torch.randn(E, generator=g)).to(DEV) if biased else None
+    rows = torch.arange(0, T, max(1, T // 104), device=DEV)
+    rows = torch.cat([rows, torch.arange(16, device=DEV)])
+    for renormalize in (True, False):
+        check_route_rows(x.to(DEV), k, rows, score=score, bias=bias, renormalize=renormalize)
+
+
+@pytest.mark.parametrize("T", [300, 2100])
+@pytest.mark.parametrize("score,spread", [("sigmoid", 1e-4), ("softmax", 1e-2)])
+@pytest.mark.parametrize("level", [3.0, 25.0, 100.0, -1000.0, 3e4, 4e6])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_route_groups_of_large_choices(T, score, spread, level, group_score):
+    """Biases that leave few of a choice's bits to the score: the choices, and sums of two, are closer
+    than fp32 tells apart, and the order has to be that of 64 bits."""
+    E = 128
+    g = torch.Generator().manual_seed(T)
+    x = (spread * torch.randn(T, E, generator=g)).to(DEV)
+    bias = torch.full((E,), level, device=DEV)
+    rows = torch.cat([torch.arange(100), torch.arange(T - 20, T)]).to(DEV)
+    check_route_rows(x, 6, rows, score=score, bias=bias, n_groups=8, top_groups=3, group_score=group_score)

@@ -413,56 +413,48 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(RouteArgs r) {
     }
   }
 
-  // ---- all of it in fp64, where fp32 did not settle the order (wave-uniform)
-  if (__ballot(unsure)) {
-    const double z = softmax ? denom64() : 1.0;
-    double wide[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      wide[v] = kNegInfD;
-      if (x[v] > kNegInf) {
-        if constexpr (BIASED) {
-          const double c = score64(softmax, x[v], (double)top, z) + (double)r.bias[v * L + lane];
-          if (c > kNegInfD) wide[v] = c;
-        } else {
-          wide[v] = (double)x[v];
-        }
-      }
-    }
-    if (r.groups > 1) {
-      asm volatile("" ::: "memory");
+  // ---- all of it in fp64, where fp32 did not settle the order of biased choices (wave-uniform)
+  if constexpr (BIASED) {
+    if (__ballot(unsure)) {
+      const double z = softmax ? denom64() : 1.0;
+      double wide[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        double c = wide[v];
-        if constexpr (!BIASED) {
-          if (r.group_score == 1 && c > kNegInfD) c = score64(softmax, x[v], (double)top, z);
+        wide[v] = kNegInfD;
+        if (x[v] > kNegInf) {
+          const double c = score64(softmax, x[v], (double)top, z) + (double)r.bias[v * L + lane];
+          if (c > kNegInfD) wide[v] = c;
         }
-        choice_lds[sub][v * L + lane] = c;
       }
-      asm volatile("" ::: "memory");
-      bool never = false;
-      const uint64_t kept = kept_groups<L, double>(r, per, choice_lds[sub], group_lds[sub], lane, 0.0, never);
+      if (r.groups > 1) {
+        asm volatile("" ::: "memory");
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (!((kept >> std::min(small_div(v * L + lane, inverse_per), 63)) & 1)) wide[v] = kNegInfD;
+        for (int v = 0; v < V; ++v) choice_lds[sub][v * L + lane] = wide[v];
+        asm volatile("" ::: "memory");
+        bool never = false;
+        const uint64_t kept = kept_groups<L, double>(r, per, choice_lds[sub], group_lds[sub], lane, 0.0, never);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (!((kept >> std::min(small_div(v * L + lane, inverse_per), 63)) & 1)) wide[v] = kNegInfD;
+      }
+      double best, value;
+      int at;
+      lane_best<V>(wide, kNegInfD, best, at);
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) my_id[q] = -1;
+      for (int j = 0; j < r.k; ++j) {
+        const int id = take_best<L, V>(wide, kNegInfD, best, at, lane, value);
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (j == q * L + lane) my_id[q] = id;
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const float xi = my_id[q] >= 0 ? load_logit<DT>(r.logits, t * r.ldl + my_id[q]) : kNegInf;
+        my_w[q] = score64(softmax, xi, (double)top, z);
+      }
+      rank0 = lane;
     }
-    double best, value;
-    int at;
-    lane_best<V>(wide, kNegInfD, best, at);
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) my_id[q] = -1;
-    for (int j = 0; j < r.k; ++j) {
-      const int id = take_best<L, V>(wide, kNegInfD, best, at, lane, value);
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q)
-        if (j == q * L + lane) my_id[q] = id;
-    }
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
-      const float xi = my_id[q] >= 0 ? load_logit<DT>(r.logits, t * r.ldl + my_id[q]) : kNegInf;
-      my_w[q] = score64(softmax, xi, (double)top, z);
-    }
-    rank0 = lane;
   }
 
   // ---- weights: over their sum where asked (0 where that is 0), times the factor

@@ -255,3 +255,112 @@ def test_route_groups_of_large_choices(T, score, spread, level, group_score):
     bias = torch.full((E,), level, device=DEV)
     rows = torch.cat([torch.arange(100), torch.arange(T - 20, T)]).to(DEV)
     check_route_rows(x, 6, rows, score=score, bias=bias, n_groups=8, top_groups=3, group_score=group_score)
+
+
+# ---------------------------------------------------------------- plan
+@pytest.mark.parametrize("T,k,E", [(100, 4, 16), (5000, 4, 33), (80000, 8, 60)])
+def test_plan_with_the_callers_workspace(T, k, E):
+    ids = torch.randint(-1, E + 1, (T, k), dtype=torch.int32, device=DEV, generator=torch.Generator(device=DEV).manual_seed(T))
+    want = pql.moe_plan(ids, E)
+    need = pql._plan_workspace(T, k, E)
+    ws = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = pql.moe_plan(ids, E, workspace=ws)
+    again = pql.moe_plan(ids, E, workspace=ws)                # dirty from the first
+    for f in ("offsets", "order", "slots"):
+        assert torch.equal(getattr(got, f), getattr(want, f)) and torch.equal(getattr(again, f), getattr(want, f))
+    assert (ws[need:] == 0x5A).all()
+    if need:
+        with pytest.raises(ValueError, match="workspace"):
+            pql.moe_plan(ids, E, workspace=ws[:need - 1])
+        with pytest.raises(ValueError, match="aligned"):
+            pql.moe_plan(ids, E, workspace=ws[8:])
+    with pytest.raises(ValueError, match="workspace"):
+        pql.moe_plan(ids, E, workspace=torch.empty(need, dtype=torch.uint8))
+
+
+# ---------------------------------------------------------------- together
+def _layer(scheme, E, hidden, width, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    w_in = (0.05 * torch.randn(E * 2 * width, hidden, device=DEV, generator=g)).bfloat16()
+    w_out = (0.05 * torch.randn(E * hidden, width, device=DEV, generator=g)).bfloat16()
+    return pql.quantize(w_in, scheme, "weight"), pql.quantize(w_out, scheme, "weight")
+
+
+SIZES = [(3, 2, 64), (300, 2, 8), (2400, 4, 130), (9000, 2, 6)]   # the streams, tiles of 128 and of 256 rows
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("T,k,E", SIZES)
+def test_layers_at_once(scheme, T, k, E):
+    """Two layers on two streams at the same time, several times over: each gives what it gives alone."""
+    hidden, width = 512, 768
+    wi, wo = _layer(scheme, E, hidden, width, 1)
+    inputs = []
+    for seed in (1, 2):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        x = torch.randn(T, hidden, device=DEV, generator=g).bfloat16()
+        inputs.append((x, torch.randn(T, E, device=DEV, generator=g)))
+
+    def layer(x, logits):
+        ids, weights = pql.moe_route(logits, k)
+        return pql.moe_mlp(x, ids, weights, wi, wo, E, add=x)
+
+    want = [layer(*i) for i in inputs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for s, i, out in zip(streams, inputs, got):
+            with torch.cuda.stream(s):
+                out.append(layer(*i))
+    torch.cuda.synchronize()
+    for out, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in out)
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+@pytest.mark.parametrize("T,k,E", SIZES)
+def test_layer_replayed_with_other_groups(scheme, T, k, E):
+    """Captured once; the replays see other group sizes, crowded and empty experts among them."""
+    hidden, width = 512, 768
+    wi, wo = _layer(scheme, E, hidden, width, 3)
+    x, logits = torch.zeros(T, hidden, device=DEV).bfloat16(), torch.zeros(T, E, device=DEV)
+
+    def layer():
+        ids, weights = pql.moe_route(logits, k)
+        return pql.moe_mlp(x, ids, weights, wi, wo, E)
+
+    def fill(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        x.copy_(torch.randn(T, hidden, device=DEV, generator=g))
+        logits.copy_(torch.randn(T, E, device=DEV, generator=g))
+        if seed == 2:
+            logits[:, E // 2] += 50.0                          # everybody's first choice
+        if seed == 3:
+            logits[:, 3:] = -float("inf")                      # three experts take all
+        if seed == 4:
+            logits[T // 2:] = -float("inf")                    # no expert for half of the tokens
+
+    fill(1)
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer()
+    for seed in (2, 3, 4, 1, 2):
+        fill(seed)
+        want = layer().clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and out.isfinite().all()
+
+
+@pytest.mark.parametrize("scheme", ["fp8_row", "fp8_block128"])
+def test_layer_of_no_tokens_and_of_no_local_experts(scheme):
+    wi, wo = _layer(scheme, 2, 128, 256, 1)
+    none = torch.empty(0, 2, dtype=torch.int32, device=DEV)
+    assert pql.moe_mlp(torch.empty(0, 128, device=DEV).bfloat16(), none, none.float(), wi, wo, 2).shape == (0, 128)
+    x = torch.randn(33, 128, device=DEV).bfloat16()
+    ids = torch.full((33, 2), 5, dtype=torch.int32, device=DEV)   # all on other ranks
+    out = pql.moe_mlp(x, ids, torch.ones(33, 2, device=DEV), wi, wo, 2, add=x)
+    assert torch.equal(out, x)

@@ -390,8 +390,8 @@ pql_status pql_moe_qgemm(int scheme, const void* a, const void* a_scales, int64_
 /* Gated activation and quantization in one pass, FP8_ROW and FP8_BLOCK128:
  *   h[r, c] = silu(x[r, c]) * x[r, cols + c],  silu(g) = g / (1 + exp(-g)),
  * from a bf16 [rows, 2 * cols] tensor (gate half, then up half; row stride ldx),
- * kept in fp32, then quantized by the scheme's activation rule into codes and
- * scales as pql_quantize lays them out.  row_count (device int32, or NULL): rows
+ * kept in fp32, then quantized by the scheme's activation rule into codes (saturating,
+ * also where a scale is subnormal) and scales as pql_quantize lays them out.  row_count (device int32, or NULL): rows
  * from *row_count on are left as they were -- offsets + E of a plan, so that
  * positions of experts held elsewhere cost nothing.  h must be finite.  rows <= 2^24 - 1;
  * rows = 0 is a no-op. */

@@ -607,7 +607,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
               n_groups: int = 1, top_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
               scale: float = 1.0):
     """The ``top_k`` experts of each token, best first, and their weights: int32 and float32
-    [T, top_k] from router logits [T, E] (fp32, bf16 or fp16; any row stride).
+    [T, top_k] from router logits [T, E] (fp32, bf16 or fp16; any row stride from E on).
 
     ``score``: "softmax" or "sigmoid".  ``bias`` (float32 [E]) is added to the scores for the
     choice alone.  With ``n_groups`` > 1 only the ``top_groups`` best groups of E / n_groups

@@ -168,26 +168,34 @@ __global__ __launch_bounds__(kThreads, EU) void k_moe_stream(MoeGemmArgs g) {
 }  // namespace
 
 // Which kernel, from the sizes alone (the groups' sizes stay on the device): rows per tile, or
-// minus the row blocks of a streaming pass.  Times in us with block-128 scales, evenly routed:
-//   rows per expert          2      4      8     16     32     64    128    256
+// minus the row blocks of a streaming pass.  Times in us with block-128 scales, the same number of
+// rows for every expert, three weights in turn (none is left in a cache):
+//   rows per expert          2      4      8     16     32     64    128    256   1024
 //   E = 64, N = 4096, K = 2048 (1024 tiles and more)
-//     stream, 1 block       62     76    106    154    256
-//     tiles of 128          77     97    100    104    114
-//   E = 16, N = 2816, K = 2048 (176 tiles)
-//     stream, 1 / 4 blocks  17     --     21     31     43     71    122
-//     tiles of 128          20     --     26     26     27     29     50
-//   E = 8, N = 1024, K = 2048 (32 tiles)
-//     stream, 4 blocks                            9     13     19     28     44
-//     tiles of 128                               17     21     24     25     26
-//   E = 4, N = 4096, K = 2048 (64 tiles)
-//     stream, 4 blocks                           13     17     26     42     78
-//     tiles of 128                               17     20     23     26     27
+//     stream, 1 block       87     88     94    114    199
+//     tiles of 128         101    101    102    105    109     --    142     --    776
+//     tiles of 256         107    107    108    110    113     --    142     --    644
+//   E = 16, N = 2816, K = 2048 (176 tiles and more)
+//     stream, 1 / 4 blocks  19     --     20     23     40     59    108    207
+//     tiles of 128          25     --     25     25     26     28     31     54
+//     tiles of 256          26     --     26     26     27     28     31     41
+//   E = 8, N = 1024, K = 2048 (32 tiles and more)
+//     stream, 4 blocks                            7      9     12     22     40
+//     tiles of 128                               17     17     20     24     25
+//   E = 4, N = 4096, K = 2048 (64 tiles and more)
+//     stream, 4 blocks                           12     15     22     39     72
+//     tiles of 128                               17     17     21     25     26
 // A tile reads a weight once for 128 rows; the stream reads it once per pass (16 or 64 rows), but
 // spreads an expert over N / 32 workgroups and more, so it holds on longer where tiles leave CUs
 // idle: up to 2^19 outputs at 32 rows per expert and more, whatever K (512, 2048 and 8192
-// measured: at worst 9 % over the better there), and below 2048 rows over tiles.
-// Tiles of 256 rows read the weight half as often and win where both shapes fill the chip (65536
-// rows, 64 experts, N = 4096, K = 2048: 714 against 807; 16 experts of 128 rows, N = 2816: 41 against 37).
+// measured: at worst 9 % over the better there), and below 2048 rows over tiles.  The border at 6
+// rows costs up to 11 % (16 experts of 16 rows).
+// Tiles of 256 rows read the weight half as often (64 experts of 1024 rows with row scales: 582
+// against 665).  With fewer than 512 of them a last round is nearly empty: 16 experts of 64 rows, N =
+// 2816, row scales take 29 against 23, though block scales and 256 rows 41 against 54.
+// Only the mean is known here: an expert far above it is walked by the same N / 32 workgroups of the
+// stream, and its weight read again for every 16 rows (512 x 2 assignments of 256 experts, N = 1024, K =
+// 2048: 91 us evenly routed, 158 with half of them on one expert; N = 2048, K = 4096: 354 and 401).
 static int kernel_choice(int64_t P, int64_t E, bool gather, int64_t a_rows, int64_t N, int64_t K) {
   const int64_t active = std::min(P, E), per = P / active, tiles_n = (N + 255) / 256;
   const int64_t tiles = (P / 128 + active) * tiles_n;

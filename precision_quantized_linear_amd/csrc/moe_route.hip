@@ -25,8 +25,8 @@ namespace pql {
 namespace {
 
 constexpr int kRouteThreads = 256;
-// Up to this many tokens a wave takes one token (E = 256 with bias and groups: 2048 tokens 8.2 us
-// a launch against 10.4 with four tokens a wave, 8192 tokens 19.3 against 13.7).
+// Up to this many tokens a wave takes one token (E = 256 with bias and groups: 2048 tokens 7.7 us
+// a launch against 8.1 with two tokens a wave, 4096 tokens 10.0 against 9.3).
 constexpr int64_t kRouteWide = 2048;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr double kNegInfD = -__builtin_huge_val();
@@ -489,7 +489,7 @@ hipError_t launch_route_shape(const RouteArgs& r, hipStream_t st) {
 
 // 16 lanes per token while a lane then holds at most 16 logits: a round's reductions serve four
 // tokens of a wave at once (32 lanes for 129 - 256 experts with a bias, whose fp64 tail is then
-// shorter: 8192 tokens 12.9 us against 14.6).  Few tokens take a wave each: shorter chains.
+// shorter: 4096 tokens 9.3 us against 10.7, 8192 tokens 12.4 against 11.9).  Few tokens take a wave each: shorter chains.
 template <int DT, bool BIASED>
 hipError_t launch_route_type(const RouteArgs& r, hipStream_t st) {
   if (r.T <= kRouteWide) {
@@ -513,8 +513,8 @@ hipError_t launch_route_type(const RouteArgs& r, hipStream_t st) {
 // per wave and expert in LDS that only this wave touches, so no atomics and no order to lose).
 // Up to kPlanChunk assignments take one launch of one workgroup; more take two: k_moe_count
 // writes each chunk's counts, and every workgroup of k_moe_place sums those of all chunks and
-// of the chunks before its own.  Latency throughout: 144 assignments 3.4 us, 65536 of 256
-// experts 9.5.
+// of the chunks before its own.  Latency throughout: 144 assignments 3.2 us, 65536 of 256
+// experts 9.2.
 constexpr int kPlanThreads = 512, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanChunk = 2048;
 constexpr int kPlanMaxBlocks = 256;   // beyond 2^19 assignments the chunks grow instead

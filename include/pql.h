@@ -26,8 +26,9 @@
  *   - Launch log: with the environment variable PQL_LOG set to anything but
  *     "" or "0" (read once, at the first call), pql_quantize,
  *     pql_quantize_static, pql_dequantize, pql_qgemm(_ex), pql_qlinear(_ex),
- *     pql_qlinear_noalloc, pql_repack and the expert calls (pql_moe_*,
- *     pql_swiglu_quantize) each write one line to stderr: the
+ *     pql_qlinear_noalloc, pql_repack, the expert calls (pql_moe_*,
+ *     pql_swiglu_quantize) and those of the cache (pql_rope, pql_kv_*) each
+ *     write one line to stderr: the
  *     call, scheme, role and shape, then the kernel enqueued (the name
  *     pql_kernel_name gives) and the stream, "nothing to do" for an empty
  *     operand, or "rejected (status S)" with the pql_last_error() text.
@@ -409,6 +410,120 @@ pql_status pql_moe_combine(const void* y, int64_t y_rows, int64_t ldy, const int
 
 /* Name of the kernel pql_moe_qgemm would launch; "" if the combination is invalid. */
 const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+
+/* -------------------------------------------------- cache of keys and values
+ * The attention of a layer beside its quantized linears: q and k are turned by
+ * their positions, k and v go into a paged cache, quantized as they are written
+ * ("[vLLM] Other quantization: FP8, ModelOpt, INC, TorchAO, Quark", section
+ * "ModelOpt": KV-cache quantization), and the new tokens attend over the pages.
+ * Per layer and step:
+ *   pql_rope (q) -> pql_kv_append (k, v) -> pql_kv_attention
+ * with pql_kv_slots once per step.  Nothing is read back to the host, so a
+ * step can be captured into a HIP graph.
+ *
+ * A cache holds n_pages pages of page_size tokens (a power of two, 16 .. 2^16;
+ * n_pages * page_size <= 2^31 - 1) for Hk heads of D values, D one of 64, 128,
+ * 192, 256:
+ *   KV_BF16        k, v bf16 [n_pages, Hk, page_size, D]            no scales
+ *   KV_FP8_TENSOR  k, v e4m3fn codes of the same shape              scales f32 [1] each,
+ *                                                                   given by the caller
+ *   KV_FP8_ROW     k, v e4m3fn codes of the same shape              scales f32 [n_pages, Hk, page_size]
+ * (FP8: the rules of the schemes of that name, a row being one token's head.)
+ * Token slot s is place s % page_size of page s / page_size.  Nothing in a
+ * cache needs to be initialised: a slot that no token was written to is never
+ * part of an answer.
+ *
+ * A batch is B sequences: the new tokens of sequence b are the rows
+ * starts[b] .. starts[b + 1] - 1 of q, k and v (starts int32 [B + 1], not
+ * decreasing), lens[b] (int32) is its number of tokens in the cache with the
+ * new ones, and pages[b, p] (int32 [B, width], row stride ldp >= width) the
+ * page of its tokens p * page_size on.  The i-th of n new tokens is at
+ * position lens[b] - n + i.  Values outside their ranges are never followed:
+ * starts are cut to 0 .. T, negative lens to 0, and tokens past the width pages
+ * or on a page outside 0 .. n_pages - 1 are absent.
+ * Row strides ld*t (token) and ld*h (head) are in elements, any multiples of 8;
+ * the D values of a head are contiguous and start on 16 bytes.  T * H <= 2^31 - 1,
+ * B <= 2^20, width * page_size <= 2^30. */
+
+typedef enum pql_kv_scheme { PQL_KV_BF16 = 0, PQL_KV_FP8_TENSOR = 1, PQL_KV_FP8_ROW = 2 } pql_kv_scheme;
+
+/* Which values of a head form the pairs that are turned: (i, i + rotary / 2),
+ * or (2 i, 2 i + 1). */
+typedef enum pql_rope_layout { PQL_ROPE_HALF = 0, PQL_ROPE_INTERLEAVED = 1 } pql_rope_layout;
+
+/* Rotary positions: the first `rotary` values of every head of x[T, H, D] are
+ * turned pair by pair,
+ *   (x1, x2) -> scale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *   a = positions[t] * freqs[i] radians,
+ * the others copied.  freqs: device fp64 [rotary / 2]; the angle is formed and
+ * reduced in fp64, so positions far out keep theirs, the rest is fp32 with one
+ * rounding to bf16.  out may be x itself with the same strides (no other
+ * overlap).  rotary: a multiple of 16 up to D, D a multiple of 8 up to 1024;
+ * positions int32.  T = 0 is a no-op. */
+pql_status pql_rope(int layout, const void* x, int64_t T, int64_t H, int64_t D, int64_t ldxt, int64_t ldxh,
+                    const int32_t* positions, const double* freqs, int64_t rotary, float scale, void* out,
+                    int64_t ldot, int64_t ldoh, void* stream);
+
+/* Byte sizes of each of a cache's two codes buffers and of its two scales
+ * buffers (host outputs, either may be NULL). */
+pql_status pql_kv_sizes(int scheme, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D, size_t* codes_bytes,
+                        size_t* scales_bytes);
+
+/* slots[t] and positions[t] (int32 [T]) of a batch's new tokens.  Rows of no
+ * sequence get slot -1 and position 0, as does a token before the start of its
+ * sequence (more new tokens than lens[b]); a token past its row of pages or on a
+ * negative page gets slot -1. */
+pql_status pql_kv_slots(const int32_t* starts, const int32_t* lens, const int32_t* pages, int64_t B, int64_t width,
+                        int64_t ldp, int64_t page_size, int64_t T, int32_t* slots, int32_t* positions, void* stream);
+
+/* Write T tokens' keys and values into the slots[t] of a cache.  A slot
+ * outside 0 .. n_pages * page_size - 1 writes nothing (padding); a slot named
+ * twice holds one of its two tokens' values in each byte, which is not said.
+ * With positions (int32 [T]; NULL: none) the keys are turned first, as pql_rope
+ * does, and quantized from fp32 without a rounding in between; layout, freqs,
+ * rotary and rope_scale as there.
+ * KV_FP8_TENSOR reads its scales (finite and positive), KV_FP8_ROW writes them:
+ * s = fp32(amax / 448) over the head (1 if 0), code = e4m3fn(fp32(x / s)),
+ * saturating.  A NaN stays a NaN (and an infinity makes its row NaN under
+ * KV_FP8_ROW). */
+pql_status pql_kv_append(int scheme, const void* k, int64_t ldkt, int64_t ldkh, const void* v, int64_t ldvt,
+                         int64_t ldvh, int64_t T, const int32_t* slots, int layout, const int32_t* positions,
+                         const double* freqs, int64_t rotary, float rope_scale, void* k_codes, void* v_codes,
+                         float* k_scales, float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                         void* stream);
+
+/* The keys and values of n slots back in bf16, bf16_RNE(fp32(decode(code) * s)),
+ * as k_out and v_out [n, Hk, D].  A slot outside the cache reads as zeros. */
+pql_status pql_kv_read(int scheme, const void* k_codes, const void* v_codes, const float* k_scales,
+                       const float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                       const int32_t* slots, int64_t n, void* k_out, int64_t ldkt, int64_t ldkh, void* v_out,
+                       int64_t ldvt, int64_t ldvh, void* stream);
+
+/* Workspace bytes of pql_kv_attention (host output; may be 0). */
+pql_status pql_kv_attention_workspace(int scheme, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t B,
+                                      int64_t width, int64_t page_size, size_t* bytes);
+
+/* Attention of a batch's new tokens over its pages, H query heads of which
+ * H / Hk consecutive ones share a head of the cache:
+ *   out[t, h] = sum_j p_j v_j,  p = softmax over the visible j of scale * q[t, h] . k_j
+ * j runs over the sequence's tokens; with causal != 0 a token at position i
+ * sees j <= i, with window > 0 only j > i - window.  q: bf16 [T, H, D]; scores,
+ * sums and the joining of a split context are fp32, the weights p enter the
+ * matrix cores in 16 bits (fp16 for FP8 caches, bf16 for KV_BF16), one rounding to bf16 at
+ * the end.  lse (fp32 [T, H], contiguous, or NULL) receives log sum_j exp(scale q . k_j).
+ * A token that sees nothing gets zeros and an lse of -inf.  Rows of no sequence
+ * are left as they were.  A NaN or an infinity in the cache reaches only
+ * the tokens that see it, possibly all of their D values. */
+pql_status pql_kv_attention(int scheme, const void* q, int64_t ldqt, int64_t ldqh, int64_t T, int64_t H,
+                            const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                            int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D, const int32_t* starts,
+                            const int32_t* lens, const int32_t* pages, int64_t B, int64_t width, int64_t ldp,
+                            int causal, int64_t window, float scale, void* out, int64_t ldot, int64_t ldoh, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Name of the kernel pql_kv_attention would launch; "" if the combination is invalid. */
+const char* pql_kv_kernel_name(int scheme, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t B, int64_t width,
+                               int64_t page_size);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,8 @@ There is no CPU fallback: if the library is missing, every call raises.
 
 A layer of experts (``moe_route``, ``moe_plan``, ``moe_qgemm``, ``swiglu_quantize``,
 ``moe_combine``, and all of them after the router as ``moe_mlp``) is for inference like the
-rest: no call records a gradient.
+rest: no call records a gradient.  So is the cache of keys and values with the attention over it
+(``rope``, ``kv_slots``, ``kv_append``, ``kv_read``, ``kv_attention``; ``kv.py``).
 """
 from __future__ import annotations
 
@@ -77,7 +78,19 @@ def lib() -> ctypes.CDLL:
         L.pql_moe_qgemm.argtypes = [ci, vp, vp, i64, ci, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp]
         L.pql_swiglu_quantize.argtypes = [ci, vp, i64, i64, i64, vp, vp, vp, vp]
         L.pql_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp, i64, vp]
-        for f in ("pql_moe_route", "pql_moe_plan_workspace", "pql_moe_plan", "pql_moe_qgemm", "pql_swiglu_quantize",
+        L.pql_rope.argtypes = [ci, vp, i64, i64, i64, i64, i64, vp, vp, i64, f32, vp, i64, i64, vp]
+        L.pql_kv_sizes.argtypes = [ci, i64, i64, i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.pql_kv_slots.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp]
+        L.pql_kv_append.argtypes = [ci, vp, i64, i64, vp, i64, i64, i64, vp, ci, vp, vp, i64, f32, vp, vp, vp, vp, i64,
+                                    i64, i64, i64, vp]
+        L.pql_kv_read.argtypes = [ci, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp]
+        L.pql_kv_attention_workspace.argtypes = [ci, i64, i64, i64, i64, i64, i64, i64, ctypes.POINTER(sz)]
+        L.pql_kv_attention.argtypes = [ci, vp, i64, i64, i64, i64, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, i64,
+                                       i64, i64, ci, i64, f32, vp, i64, i64, vp, vp, sz, vp]
+        L.pql_kv_kernel_name.restype = ctypes.c_char_p
+        L.pql_kv_kernel_name.argtypes = [ci, i64, i64, i64, i64, i64, i64, i64]
+        for f in ("pql_rope", "pql_kv_sizes", "pql_kv_slots", "pql_kv_append", "pql_kv_read",
+                  "pql_kv_attention_workspace", "pql_kv_attention", "pql_moe_route", "pql_moe_plan_workspace", "pql_moe_plan", "pql_moe_qgemm", "pql_swiglu_quantize",
                   "pql_moe_combine", "pql_quantized_sizes", "pql_workspace_size", "pql_quantize", "pql_dequantize",
                   "pql_qgemm", "pql_qlinear", "pql_quantize_static", "pql_qgemm_ex", "pql_qlinear_ex",
                   "pql_qlinear_noalloc", "pql_layout_sizes", "pql_repack"):
@@ -785,3 +798,7 @@ def moe_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w_in: QTe
         h = moe_qgemm(quantize(x, w_in.scheme), w_in, plan, gather=True)
         y = moe_qgemm(swiglu_quantize(h, w_in.scheme, plan), w_out, plan)
         return moe_combine(y, plan, weights, add=add)
+
+
+from .kv import (KV_HEAD_DIMS, KV_SCHEMES, ROPE_LAYOUTS, KVCache, Rope, kv_append, kv_attention,   # noqa: E402,F401
+                 kv_attention_workspace, kv_cache, kv_kernel_name, kv_read, kv_sizes, kv_slots, rope, rope_freqs)

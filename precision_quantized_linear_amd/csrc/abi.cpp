@@ -1069,3 +1069,413 @@ pql_status pql_moe_combine(const void* y, int64_t y_rows, int64_t ldy, const int
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- cache of keys and values
+// Rotary positions, slots, append, read and the attention over a paged cache.
+namespace {
+
+constexpr int64_t kKvMaxBatch = int64_t(1) << 20;
+constexpr int64_t kInt31 = (int64_t(1) << 31) - 1;
+
+// Rows of heads [n, H, D], 8 values a thread: a launch has at most 2^32 - 1 threads along an axis.
+pql_status check_heads(const char* n_name, int64_t n, const char* h_name, int64_t H, int64_t D) {
+  if (n < 0) return fail(PQL_ERR_INVALID_ARGUMENT, "%s must be >= 0 (got %lld)", n_name, (long long)n);
+  if (H < 1 || H > kInt31) return fail(PQL_ERR_INVALID_ARGUMENT, "%s must be 1 .. 2^31 - 1 (got %lld)", h_name, (long long)H);
+  if (n > kInt31 / H)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%s * %s above 2^31 - 1 is not supported (got %lld * %lld)", n_name, h_name,
+                (long long)n, (long long)H);
+  if (n * H > (int64_t(1) << 34) / D)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%lld x %lld heads of %lld values are too large", (long long)n, (long long)H,
+                (long long)D);
+  return PQL_OK;
+}
+
+// Strides of a [n, H, D] operand: multiples of 8, heads that do not overlap, in reach.
+pql_status check_head_strides(const char* name, int64_t ldt, int64_t ldh, int64_t n, int64_t H, int64_t D) {
+  if (ldt < 0 || ldh < 0 || ldt % 8 || ldh % 8)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 and not negative (got %lld, %lld)", name,
+                (long long)ldt, (long long)ldh);
+  const int64_t rows = n > 0 ? n - 1 : 0;
+  if ((rows && ldt > kMaxSpan / rows) || (H > 1 && ldh > kMaxSpan / (H - 1)) || rows * ldt + (H - 1) * ldh + D > kMaxSpan)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%s spans more than 2^40 elements", name);
+  return PQL_OK;
+}
+
+// An operand that is written: no head may lie over another.
+pql_status check_written(const char* name, int64_t ldt, int64_t ldh, int64_t n, int64_t H, int64_t D) {
+  const bool apart = (H == 1 || ldh >= D) && (n <= 1 || ldt >= (H - 1) * ldh + D);        // [token][head]
+  const bool swapped = (n <= 1 || ldt >= D) && (H == 1 || ldh >= (n - 1) * ldt + D);      // [head][token]
+  if (!apart && !swapped)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%s: rows overlap (strides %lld, %lld)", name, (long long)ldt, (long long)ldh);
+  return PQL_OK;
+}
+
+pql_status check_cache(int scheme, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D) {
+  if (scheme != PQL_KV_BF16 && scheme != PQL_KV_FP8_TENSOR && scheme != PQL_KV_FP8_ROW)
+    return fail(PQL_ERR_UNSUPPORTED, "unknown cache scheme %d", scheme);
+  if (D != 64 && D != 128 && D != 192 && D != 256)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "a cache's head size must be 64, 128, 192 or 256 (got %lld)", (long long)D);
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "page_size must be a power of two, 16 .. 65536 (got %lld)", (long long)page_size);
+  if (n_pages < 1 || n_pages > kInt31 / page_size)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "n_pages must be 1 .. (2^31 - 1) / page_size (got %lld)", (long long)n_pages);
+  if (Hk < 1 || Hk > kMaxSpan / (n_pages * page_size * D))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "a cache of %lld x %lld x %lld x %lld is too large or has no heads",
+                (long long)n_pages, (long long)Hk, (long long)page_size, (long long)D);
+  return PQL_OK;
+}
+
+pql_status check_cache_buffers(int scheme, const void* k, const void* v, const float* ks, const float* vs) {
+  if (!k || !v) return fail(PQL_ERR_INVALID_ARGUMENT, "k_codes and v_codes must be non-NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(PQL_ERR_INVALID_ARGUMENT, "k_codes and v_codes must be 16-byte aligned");
+  if (scheme == PQL_KV_BF16) return PQL_OK;
+  if (!ks || !vs) return fail(PQL_ERR_INVALID_ARGUMENT, "an FP8 cache needs k_scales and v_scales");
+  if (!aligned16(ks) || !aligned16(vs))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "k_scales and v_scales must be 16-byte aligned");
+  return PQL_OK;
+}
+
+pql_status check_batch(int64_t B, int64_t width, int64_t ldp, int64_t page_size) {
+  if (B < 0 || B > kKvMaxBatch) return fail(PQL_ERR_INVALID_ARGUMENT, "B must be 0 .. 2^20 (got %lld)", (long long)B);
+  if (width < 0 || width > (int64_t(1) << 30) / page_size)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "width must be 0 .. 2^30 / page_size (got %lld)", (long long)width);
+  if (ldp < width || (B > 1 && ldp > kMaxSpan / (B - 1)))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "ldp must be >= width = %lld and in reach (got %lld)", (long long)width,
+                (long long)ldp);
+  return PQL_OK;
+}
+
+pql_status check_turn(int layout, const int32_t* positions, const double* freqs, int64_t rotary, float scale, int64_t D) {
+  if (layout != PQL_ROPE_HALF && layout != PQL_ROPE_INTERLEAVED)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "unknown rotary layout %d", layout);
+  if (rotary < 16 || rotary % 16 || rotary > D)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "rotary must be a multiple of 16, 16 .. D = %lld (got %lld)", (long long)D,
+                (long long)rotary);
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(PQL_ERR_INVALID_ARGUMENT, "the rotary scale must be finite");
+  if (!positions || !freqs) return fail(PQL_ERR_INVALID_ARGUMENT, "positions and freqs must be non-NULL");
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(freqs) & 7u))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "positions and freqs must be aligned to their elements");
+  return PQL_OK;
+}
+
+int page_shift_of(int64_t page_size) { return __builtin_ctzll((unsigned long long)page_size); }
+
+}  // namespace
+
+extern "C" {
+
+static pql_status rope_impl(int layout, const void* x, int64_t T, int64_t H, int64_t D, int64_t ldxt, int64_t ldxh,
+                            const int32_t* positions, const double* freqs, int64_t rotary, float scale, void* out,
+                            int64_t ldot, int64_t ldoh, void* stream) {
+  if (D < 16 || D > 1024 || D % 8)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "D must be a multiple of 8, 16 .. 1024 (got %lld)", (long long)D);
+  pql_status st = check_heads("T", T, "H", H, D);
+  if (st != PQL_OK) return st;
+  if ((st = check_head_strides("x", ldxt, ldxh, T, H, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("out", ldot, ldoh, T, H, D)) != PQL_OK) return st;
+  if ((st = check_written("out", ldot, ldoh, T, H, D)) != PQL_OK) return st;
+  if (T == 0) {   // the pointers of empty tensors are NULL
+    static const int32_t none = 0;
+    static const double no_freq = 0.0;
+    if ((st = check_turn(layout, &none, &no_freq, rotary, scale, D)) != PQL_OK) return st;
+    return ok();
+  }
+  if ((st = check_turn(layout, positions, freqs, rotary, scale, D)) != PQL_OK) return st;
+  if (!x || !out) return fail(PQL_ERR_INVALID_ARGUMENT, "x and out must be non-NULL");
+  if (!aligned16(x) || !aligned16(out)) return fail(PQL_ERR_INVALID_ARGUMENT, "x and out must be 16-byte aligned");
+  if (x == out && ((T > 1 && ldxt != ldot) || (H > 1 && ldxh != ldoh)))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "in place, x and out must have the same strides");
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::RopeArgs g{};
+  g.x = static_cast<const uint16_t*>(x);
+  g.out = static_cast<uint16_t*>(out);
+  g.T = T;
+  g.ldxt = ldxt;
+  g.ldxh = ldxh;
+  g.ldot = ldot;
+  g.ldoh = ldoh;
+  g.H = (int)H;
+  g.D = (int)D;
+  g.rotary = (int)rotary;
+  g.positions = positions;
+  g.freqs = freqs;
+  g.scale = scale;
+  return launched(pql::launch_rope(layout, g, static_cast<hipStream_t>(stream)), "rope launch");
+}
+
+pql_status pql_rope(int layout, const void* x, int64_t T, int64_t H, int64_t D, int64_t ldxt, int64_t ldxh,
+                    const int32_t* positions, const double* freqs, int64_t rotary, float scale, void* out,
+                    int64_t ldot, int64_t ldoh, void* stream) {
+  const pql_status st =
+      rope_impl(layout, x, T, H, D, ldxt, ldxh, positions, freqs, rotary, scale, out, ldot, ldoh, stream);
+  if (log_enabled())
+    log_moe(st, "rope", shape_text("T=%lld H=%lld D=%lld", (long long)T, (long long)H, (long long)D), T == 0, "k_rope",
+            stream);
+  return st;
+}
+
+pql_status pql_kv_sizes(int scheme, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D, size_t* codes_bytes,
+                        size_t* scales_bytes) {
+  if (codes_bytes) *codes_bytes = 0;
+  if (scales_bytes) *scales_bytes = 0;
+  const pql_status st = check_cache(scheme, n_pages, page_size, Hk, D);
+  if (st != PQL_OK) return st;
+  const size_t rows = (size_t)n_pages * (size_t)page_size * (size_t)Hk;
+  if (codes_bytes) *codes_bytes = rows * (size_t)D * (scheme == PQL_KV_BF16 ? 2 : 1);
+  if (scales_bytes) *scales_bytes = scheme == PQL_KV_BF16 ? 0 : scheme == PQL_KV_FP8_TENSOR ? 4 : 4 * rows;
+  return ok();
+}
+
+static pql_status kv_slots_impl(const int32_t* starts, const int32_t* lens, const int32_t* pages, int64_t B,
+                                int64_t width, int64_t ldp, int64_t page_size, int64_t T, int32_t* slots,
+                                int32_t* positions, void* stream) {
+  pql_status st = check_cache(PQL_KV_BF16, 1, page_size, 1, 64);
+  if (st != PQL_OK) return st;
+  if ((st = check_batch(B, width, ldp, page_size)) != PQL_OK) return st;
+  if (T < 0 || T > kInt31) return fail(PQL_ERR_INVALID_ARGUMENT, "T must be 0 .. 2^31 - 1 (got %lld)", (long long)T);
+  if (T == 0) return ok();
+  if (!slots || !positions || !starts || (B > 0 && !lens) || (B > 0 && width > 0 && !pages))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "starts, lens, pages, slots and positions must be non-NULL");
+  if (!aligned4(starts) || !aligned4(lens) || !aligned4(pages) || !aligned4(slots) || !aligned4(positions))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "starts, lens, pages, slots and positions must be 4-byte aligned");
+  if ((st = check_device()) != PQL_OK) return st;
+  return launched(pql::launch_kv_slots(starts, lens, pages, (int)B, width, ldp, page_shift_of(page_size), T, slots,
+                                       positions, static_cast<hipStream_t>(stream)),
+                  "kv_slots launch");
+}
+
+pql_status pql_kv_slots(const int32_t* starts, const int32_t* lens, const int32_t* pages, int64_t B, int64_t width,
+                        int64_t ldp, int64_t page_size, int64_t T, int32_t* slots, int32_t* positions, void* stream) {
+  const pql_status st = kv_slots_impl(starts, lens, pages, B, width, ldp, page_size, T, slots, positions, stream);
+  if (log_enabled())
+    log_moe(st, "kv_slots", shape_text("T=%lld B=%lld width=%lld", (long long)T, (long long)B, (long long)width), T == 0,
+            "k_kv_slots", stream);
+  return st;
+}
+
+static pql_status kv_append_impl(int scheme, const void* k, int64_t ldkt, int64_t ldkh, const void* v, int64_t ldvt,
+                                 int64_t ldvh, int64_t T, const int32_t* slots, int layout, const int32_t* positions,
+                                 const double* freqs, int64_t rotary, float rope_scale, void* k_codes, void* v_codes,
+                                 float* k_scales, float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk,
+                                 int64_t D, void* stream) {
+  pql_status st = check_cache(scheme, n_pages, page_size, Hk, D);
+  if (st != PQL_OK) return st;
+  if ((st = check_heads("T", T, "Hk", Hk, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("k", ldkt, ldkh, T, Hk, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("v", ldvt, ldvh, T, Hk, D)) != PQL_OK) return st;
+  if (positions && (st = check_turn(layout, positions, freqs, rotary, rope_scale, D)) != PQL_OK) return st;
+  if (T == 0) return ok();
+  if (!k || !v || !slots) return fail(PQL_ERR_INVALID_ARGUMENT, "k, v and slots must be non-NULL");
+  if (!aligned16(k) || !aligned16(v) || !aligned4(slots))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned, slots 4-byte aligned");
+  if ((st = check_cache_buffers(scheme, k_codes, v_codes, k_scales, v_scales)) != PQL_OK) return st;
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::AppendArgs g{};
+  g.k = static_cast<const uint16_t*>(k);
+  g.v = static_cast<const uint16_t*>(v);
+  g.T = T;
+  g.ldkt = ldkt;
+  g.ldkh = ldkh;
+  g.ldvt = ldvt;
+  g.ldvh = ldvh;
+  g.slots = slots;
+  g.positions = positions;
+  g.freqs = freqs;
+  g.layout = layout;
+  g.rotary = positions ? (int)rotary : 0;
+  g.rope_scale = rope_scale;
+  g.k_codes = k_codes;
+  g.v_codes = v_codes;
+  g.k_scales = k_scales;
+  g.v_scales = v_scales;
+  g.n_pages = (int)n_pages;
+  g.page_shift = page_shift_of(page_size);
+  g.Hk = (int)Hk;
+  g.D = (int)D;
+  return launched(pql::launch_kv_append(scheme, g, static_cast<hipStream_t>(stream)), "kv_append launch");
+}
+
+pql_status pql_kv_append(int scheme, const void* k, int64_t ldkt, int64_t ldkh, const void* v, int64_t ldvt,
+                         int64_t ldvh, int64_t T, const int32_t* slots, int layout, const int32_t* positions,
+                         const double* freqs, int64_t rotary, float rope_scale, void* k_codes, void* v_codes,
+                         float* k_scales, float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                         void* stream) {
+  const pql_status st =
+      kv_append_impl(scheme, k, ldkt, ldkh, v, ldvt, ldvh, T, slots, layout, positions, freqs, rotary, rope_scale,
+                     k_codes, v_codes, k_scales, v_scales, n_pages, page_size, Hk, D, stream);
+  if (log_enabled())
+    log_moe(st, "kv_append",
+            shape_text("scheme=%d T=%lld Hk=%lld D=%lld pages=%lld x %lld", scheme, (long long)T, (long long)Hk,
+                       (long long)D, (long long)n_pages, (long long)page_size),
+            T == 0, "k_kv_append", stream);
+  return st;
+}
+
+static pql_status kv_read_impl(int scheme, const void* k_codes, const void* v_codes, const float* k_scales,
+                               const float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                               const int32_t* slots, int64_t n, void* k_out, int64_t ldkt, int64_t ldkh, void* v_out,
+                               int64_t ldvt, int64_t ldvh, void* stream) {
+  pql_status st = check_cache(scheme, n_pages, page_size, Hk, D);
+  if (st != PQL_OK) return st;
+  if ((st = check_heads("n", n, "Hk", Hk, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("k_out", ldkt, ldkh, n, Hk, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("v_out", ldvt, ldvh, n, Hk, D)) != PQL_OK) return st;
+  if ((st = check_written("k_out", ldkt, ldkh, n, Hk, D)) != PQL_OK) return st;
+  if ((st = check_written("v_out", ldvt, ldvh, n, Hk, D)) != PQL_OK) return st;
+  if (n == 0) return ok();
+  if (!slots || !k_out || !v_out) return fail(PQL_ERR_INVALID_ARGUMENT, "slots, k_out and v_out must be non-NULL");
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(slots))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "k_out and v_out must be 16-byte aligned, slots 4-byte aligned");
+  if ((st = check_cache_buffers(scheme, k_codes, v_codes, k_scales, v_scales)) != PQL_OK) return st;
+  if ((st = check_device()) != PQL_OK) return st;
+  pql::ReadArgs g{};
+  g.k_codes = k_codes;
+  g.v_codes = v_codes;
+  g.k_scales = k_scales;
+  g.v_scales = v_scales;
+  g.n_pages = (int)n_pages;
+  g.page_shift = page_shift_of(page_size);
+  g.Hk = (int)Hk;
+  g.D = (int)D;
+  g.slots = slots;
+  g.n = n;
+  g.k_out = static_cast<uint16_t*>(k_out);
+  g.v_out = static_cast<uint16_t*>(v_out);
+  g.ldkt = ldkt;
+  g.ldkh = ldkh;
+  g.ldvt = ldvt;
+  g.ldvh = ldvh;
+  return launched(pql::launch_kv_read(scheme, g, static_cast<hipStream_t>(stream)), "kv_read launch");
+}
+
+pql_status pql_kv_read(int scheme, const void* k_codes, const void* v_codes, const float* k_scales,
+                       const float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                       const int32_t* slots, int64_t n, void* k_out, int64_t ldkt, int64_t ldkh, void* v_out,
+                       int64_t ldvt, int64_t ldvh, void* stream) {
+  const pql_status st = kv_read_impl(scheme, k_codes, v_codes, k_scales, v_scales, n_pages, page_size, Hk, D, slots, n,
+                                     k_out, ldkt, ldkh, v_out, ldvt, ldvh, stream);
+  if (log_enabled())
+    log_moe(st, "kv_read",
+            shape_text("scheme=%d n=%lld Hk=%lld D=%lld", scheme, (long long)n, (long long)Hk, (long long)D), n == 0,
+            "k_kv_read", stream);
+  return st;
+}
+
+// The sizes of an attention call, as far as its kernel and workspace go by them.
+static pql_status attend_shape(int scheme, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t B, int64_t width,
+                               int64_t page_size, pql::AttendArgs* g) {
+  pql_status st = check_cache(scheme, 1, page_size, Hk, D);
+  if (st != PQL_OK) return st;
+  if ((st = check_heads("T", T, "H", H, D)) != PQL_OK) return st;
+  if (H > 65535) return fail(PQL_ERR_INVALID_ARGUMENT, "H above 65535 is not supported (got %lld)", (long long)H);
+  if (H % Hk)
+    return fail(PQL_ERR_INVALID_ARGUMENT, "H = %lld must be a multiple of Hk = %lld", (long long)H, (long long)Hk);
+  if ((st = check_batch(B, width, width, page_size)) != PQL_OK) return st;
+  *g = pql::AttendArgs{};
+  g->T = T;
+  g->H = (int)H;
+  g->Hk = (int)Hk;
+  g->D = (int)D;
+  g->B = (int)B;
+  g->width = width;
+  g->page_shift = page_shift_of(page_size);
+  if (T > 0 && B > 0 && !pql::kv_attention_fits(*g))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "%lld tokens of %lld heads in %lld sequences are too many for one call",
+                (long long)T, (long long)H, (long long)B);
+  return PQL_OK;
+}
+
+pql_status pql_kv_attention_workspace(int scheme, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t B,
+                                      int64_t width, int64_t page_size, size_t* bytes) {
+  if (!bytes) return fail(PQL_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  *bytes = 0;
+  pql::AttendArgs g;
+  const pql_status st = attend_shape(scheme, T, H, Hk, D, B, width, page_size, &g);
+  if (st != PQL_OK) return st;
+  *bytes = T == 0 || B == 0 ? 0 : pql::kv_attention_ws_bytes(g);
+  return ok();
+}
+
+const char* pql_kv_kernel_name(int scheme, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t B, int64_t width,
+                               int64_t page_size) {
+  std::string text;   // the checks' own error text is not this call's
+  text.swap(g_error);
+  pql::AttendArgs g;
+  const bool valid = attend_shape(scheme, T, H, Hk, D, B, width, page_size, &g) == PQL_OK && T > 0 && B > 0;
+  text.swap(g_error);
+  return valid ? pql::kv_attention_kernel_name(g) : "";
+}
+
+static pql_status kv_attention_impl(int scheme, const void* q, int64_t ldqt, int64_t ldqh, int64_t T, int64_t H,
+                                    const void* k_codes, const void* v_codes, const float* k_scales,
+                                    const float* v_scales, int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D,
+                                    const int32_t* starts, const int32_t* lens, const int32_t* pages, int64_t B,
+                                    int64_t width, int64_t ldp, int causal, int64_t window, float scale, void* out,
+                                    int64_t ldot, int64_t ldoh, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  pql::AttendArgs g;
+  pql_status st = check_cache(scheme, n_pages, page_size, Hk, D);
+  if (st != PQL_OK) return st;
+  if ((st = attend_shape(scheme, T, H, Hk, D, B, width, page_size, &g)) != PQL_OK) return st;
+  if ((st = check_batch(B, width, ldp, page_size)) != PQL_OK) return st;
+  if (window < 0) return fail(PQL_ERR_INVALID_ARGUMENT, "window must be >= 0 (got %lld)", (long long)window);
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(PQL_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if ((st = check_head_strides("q", ldqt, ldqh, T, H, D)) != PQL_OK) return st;
+  if ((st = check_head_strides("out", ldot, ldoh, T, H, D)) != PQL_OK) return st;
+  if ((st = check_written("out", ldot, ldoh, T, H, D)) != PQL_OK) return st;
+  if (T == 0 || B == 0) return ok();
+  if (!q || !out || !starts || !lens || (width > 0 && !pages))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "q, out, starts, lens and pages must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(PQL_ERR_INVALID_ARGUMENT, "q and out must be 16-byte aligned");
+  if (!aligned4(starts) || !aligned4(lens) || !aligned4(pages) || !aligned4(lse))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "starts, lens, pages and lse must be 4-byte aligned");
+  if ((st = check_cache_buffers(scheme, k_codes, v_codes, k_scales, v_scales)) != PQL_OK) return st;
+  const size_t need = pql::kv_attention_ws_bytes(g);
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(PQL_ERR_WORKSPACE, "kv_attention needs a %zu-byte workspace (got %zu)", need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(PQL_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  }
+  if ((st = check_device()) != PQL_OK) return st;
+  g.q = static_cast<const uint16_t*>(q);
+  g.ldqt = ldqt;
+  g.ldqh = ldqh;
+  g.k_codes = k_codes;
+  g.v_codes = v_codes;
+  g.k_scales = k_scales;
+  g.v_scales = v_scales;
+  g.n_pages = (int)n_pages;
+  g.starts = starts;
+  g.lens = lens;
+  g.pages = pages;
+  g.ldp = ldp;
+  g.causal = causal != 0;
+  g.window = (int)(window > kInt31 ? 0 : window);   // a window past any length hides nothing
+  g.scale = scale;
+  g.out = static_cast<uint16_t*>(out);
+  g.ldot = ldot;
+  g.ldoh = ldoh;
+  g.lse = lse;
+  g.ws = static_cast<float*>(workspace);
+  return launched(pql::launch_kv_attention(scheme, g, static_cast<hipStream_t>(stream)), "kv_attention launch");
+}
+
+pql_status pql_kv_attention(int scheme, const void* q, int64_t ldqt, int64_t ldqh, int64_t T, int64_t H,
+                            const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                            int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D, const int32_t* starts,
+                            const int32_t* lens, const int32_t* pages, int64_t B, int64_t width, int64_t ldp,
+                            int causal, int64_t window, float scale, void* out, int64_t ldot, int64_t ldoh, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const pql_status st = kv_attention_impl(scheme, q, ldqt, ldqh, T, H, k_codes, v_codes, k_scales, v_scales, n_pages,
+                                          page_size, Hk, D, starts, lens, pages, B, width, ldp, causal, window, scale,
+                                          out, ldot, ldoh, lse, workspace, workspace_bytes, stream);
+  if (log_enabled())
+    log_moe(st, "kv_attention",
+            shape_text("scheme=%d T=%lld H=%lld Hk=%lld D=%lld B=%lld width=%lld", scheme, (long long)T, (long long)H,
+                       (long long)Hk, (long long)D, (long long)B, (long long)width),
+            T == 0 || B == 0, pql_kv_kernel_name(scheme, T, H, Hk, D, B, width, page_size), stream);
+  return st;
+}
+
+}  // extern "C"

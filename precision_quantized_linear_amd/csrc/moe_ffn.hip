@@ -60,27 +60,6 @@ __device__ __forceinline__ float absmax8(const float (&h)[8]) {
   return m;
 }
 
-__device__ __forceinline__ uint2 fp8_codes8(const float (&h)[8], float s) {
-  float q[8];
-  if (s >= kSmallestFastScale) {
-    const float rcp = __fdiv_rn(1.0f, s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = quot<true>(h[j], s, rcp);
-  } else {
-    // The statement keeps this a branch: without it both quotients are formed for every element
-    // (65536 rows of 1408 with row scales: 114 us instead of 83).
-    asm volatile("");
-    // A subnormal scale is the nearest of few steps, and a quotient can pass 464, which the convert
-    // makes a NaN (h of 656 2^-149: scale 2^-149).  A NaN h stays one.
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = quot<false>(h[j], s, 0.0f);
-      q[j] = fabsf(v) > 448.0f ? __builtin_copysignf(448.0f, v) : v;
-    }
-  }
-  return make_uint2(fp8x4(q[0], q[1], q[2], q[3]), fp8x4(q[4], q[5], q[6], q[7]));
-}
-
 __device__ __forceinline__ int64_t live_rows(const int32_t* count, int64_t rows) {
   return count ? std::min<int64_t>(rows, std::max(0, *count)) : rows;
 }

@@ -199,4 +199,69 @@ struct CombineArgs {
 // vec: every row of y, add and out starts on 16 bytes and N % 8 == 0
 hipError_t launch_moe_combine(const CombineArgs& g, bool vec, hipStream_t st);
 
+// ---------------------------------------------------------------- cache of keys and values
+struct RopeArgs {
+  const uint16_t* x;       // bf16 [T, H, D], strides ldxt, ldxh
+  uint16_t* out;
+  int64_t T, ldxt, ldxh, ldot, ldoh;
+  int H, D, rotary;
+  const int32_t* positions;
+  const double* freqs;     // fp64 [rotary / 2], radians per position
+  float scale;
+  int units, per, groups;  // set by the launcher
+};
+hipError_t launch_rope(int layout, RopeArgs g, hipStream_t st);
+
+hipError_t launch_kv_slots(const int32_t* starts, const int32_t* lens, const int32_t* pages, int B, int64_t width,
+                           int64_t ldp, int page_shift, int64_t T, int32_t* slots, int32_t* positions, hipStream_t st);
+
+struct AppendArgs {
+  const uint16_t *k, *v;   // bf16 [T, Hk, D]
+  int64_t T, ldkt, ldkh, ldvt, ldvh;
+  const int32_t* slots;
+  const int32_t* positions;   // null: the keys are not turned
+  const double* freqs;
+  int layout, rotary;
+  float rope_scale;
+  void *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  int n_pages, page_shift, Hk, D;
+  int per, groups;         // set by the launcher
+};
+hipError_t launch_kv_append(int scheme, AppendArgs g, hipStream_t st);
+
+struct ReadArgs {
+  const void *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  int n_pages, page_shift, Hk, D;
+  const int32_t* slots;
+  int64_t n;
+  uint16_t *k_out, *v_out;   // bf16 [n, Hk, D]
+  int64_t ldkt, ldkh, ldvt, ldvh;
+};
+hipError_t launch_kv_read(int scheme, const ReadArgs& g, hipStream_t st);
+
+struct AttendArgs {
+  const uint16_t* q;       // bf16 [T, H, D]
+  int64_t ldqt, ldqh, T;
+  const void *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  int n_pages, page_shift, H, Hk, D;
+  const int32_t *starts, *lens, *pages;
+  int B;
+  int64_t width, ldp;
+  int causal, window;      // window 0: none
+  float scale;
+  uint16_t* out;           // bf16 [T, H, D]
+  int64_t ldot, ldoh;
+  float* lse;              // fp32 [T, H] or null
+  float* ws;
+  int target, min_chunk, parts;   // set by the launcher: ranges in all, least key tiles of one, places per head
+};
+// These go by T, H, Hk, D, B, width and page_shift alone.
+bool kv_attention_fits(const AttendArgs& g);
+size_t kv_attention_ws_bytes(const AttendArgs& g);
+const char* kv_attention_kernel_name(const AttendArgs& g);
+hipError_t launch_kv_attention(int scheme, AttendArgs g, hipStream_t st);
+
 }  // namespace pql

@@ -64,6 +64,35 @@ __device__ __forceinline__ uint2 fp8_chunk_sat(uint4 c, float s, float rcp) {
   return make_uint2(fp8x4(f[0], f[1], f[2], f[3]), fp8x4(f[4], f[5], f[6], f[7]));
 }
 
+// 8 fp32 values -> 8 e4m3fn codes of fp32(x / s); the gated activation and the cache use it.  A NaN
+// stays one.  GIVEN: the scale is not the row's own, so that any quotient can pass 448 and saturates
+// (an infinite one, too: the corrected quotient is a NaN there).
+template <bool GIVEN = false>
+__device__ __forceinline__ uint2 fp8_codes8(const float (&h)[8], float s) {
+  float q[8];
+  if (s >= kSmallestFastScale) {
+    const float rcp = __fdiv_rn(1.0f, s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q[j] = quot<true>(h[j], s, rcp);
+      if constexpr (GIVEN)
+        if (!(fabsf(q[j]) <= 448.0f)) q[j] = h[j] != h[j] ? h[j] : __builtin_copysignf(448.0f, h[j]);
+    }
+  } else {
+    // The statement keeps this a branch: without it both quotients are formed for every element
+    // (the gated activation, 65536 rows of 1408 with row scales: 114 us instead of 83).
+    asm volatile("");
+    // A subnormal scale is the nearest of few steps, and a quotient can pass 464, which the convert
+    // makes a NaN (h of 656 2^-149: scale 2^-149).  A NaN h stays one.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = quot<false>(h[j], s, 0.0f);
+      q[j] = fabsf(v) > 448.0f ? __builtin_copysignf(448.0f, v) : v;
+    }
+  }
+  return make_uint2(fp8x4(q[0], q[1], q[2], q[3]), fp8x4(q[4], q[5], q[6], q[7]));
+}
+
 // int8 scale: s = fp32(amax / 127), 1 if that is 0.
 __device__ __forceinline__ float int8_scale(float amax) {
   float s = __fdiv_rn(amax, 127.0f);

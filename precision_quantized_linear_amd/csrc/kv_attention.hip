@@ -1,4 +1,23 @@
 // Attention of a batch's new tokens over the paged cache of keys and values, gfx950.
+//
+// For a head of the cache, the G = H / Hk query heads of n new tokens are n G rows that share its keys and
+// values.  A workgroup takes a tile of rows and a range of keys, forms
+//   S^T = K Q^T,  w = 2^(scale log2 e S - m),  O^T = V^T w^T,  l = sum w
+// with the running maximum m of a softmax, key tile by key tile, and either divides and stores, or leaves
+// (O, m, l) of its range for k_attend_join.  Both products keep keys (then head values) along the rows of
+// the matrix cores' results and the query rows along the lanes: the maximum, the sum and the correction
+// of O are one lane's own numbers, and the registers that hold w are, as they stand, the second
+// operand of the second product (its order along the keys is free, and V^T follows it).
+//
+// FP8 codes are multiplied as they are: keys in bf16 beside q, values in fp16 beside w, both exact.  With
+// a scale per token, the score of key j is s_j = ks_j (code_j . q), and its value's scale goes into the weight as a
+// power of two: w_j = 2^(s_j + log2 vs_j - m) is at most about 1 whatever the scales, O sums w_j code_j and l
+// sums w_j / vs_j, so that O / l is the answer, at one exponential per score.  w is shifted up
+// by 2^7 (and may rise 2^8 above the last m that was taken, below), so that fp16 keeps 11 bits of every weight
+// down to 2^-21 of the largest.  bf16 caches have w in bf16; there l sums the rounded weights, so that a
+// token that holds nearly all of the weight comes out without their rounding, and a second sum, of the weights
+// before they are rounded, is kept for the logarithm where it is asked for.
+// m follows the maximum only when that passes it by 2^8: O is rarely rescaled.
 #include <algorithm>
 #include <cmath>
 
@@ -11,117 +30,1070 @@ namespace pql {
 
 namespace {
 
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRise = 8.0f;       // m follows the maximum when that is so much higher
+constexpr float kSmallestValueScale = 0x1p-100f;
+
 template <int SCHEME>
-__device__ __forceinline__ void row8(const void* codes, int64_t row, int D, int c, float s, float (&f)[8]) {
-  if constexpr (SCHEME == kKvBf16) {
-    chunk_to_f32(ldg16(static_cast<const uint16_t*>(codes) + row * D + c), f);
-  } else {
-    fp8x8_to_f32(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(codes) + row * D + c), f);
+constexpr float weight_shift() { return SCHEME == kKvBf16 ? 0.0f : 7.0f; }
+
+// ---------------------------------------------------------------- work of a workgroup
+// Tiles of BM rows; keys in tiles of 64.  A sequence's row tiles are each cut into `splits` ranges of `chunk`
+// key tiles, the chunk chosen on the device so that all ranges of all heads are about `target`: long
+// contexts are spread over the card whatever the others' lengths.  Every workgroup finds its own sequence by
+// a scan over the batch, 4 sequences per lane and step.
+constexpr int kKeyTile = 64;
+
+struct Work {
+  Seq s;
+  int b, tile, split, splits, chunk;   // splits: of the sequence; a tile may need fewer
+  uint32_t part;                       // place of its range among those of a head
+};
+
+struct Shape {
+  int rows, qt, kt;   // rows of one head, row tiles, key tiles that any of them sees
+};
+
+template <int BM>
+__device__ __forceinline__ Shape shape_of(const AttendArgs& g, const Seq& s) {
+  Shape r;
+  const int64_t rows = (int64_t)s.n * (g.H / g.Hk);   // below 2^31: T H is
+  r.rows = (int)rows;
+  r.qt = (int)((rows + BM - 1) / BM);
+  const int64_t end = std::min<int64_t>(s.len, g.width << g.page_shift);
+  const int64_t begin = g.window ? std::max<int64_t>(0, (int64_t)s.len - s.n - g.window + 1) : 0;
+  const int64_t kt = (end + kKeyTile - 1) / kKeyTile - begin / kKeyTile;
+  r.kt = (int)std::max<int64_t>(0, kt);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t scan_add(uint32_t v, int lane) {   // inclusive, over the wave
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] *= s;
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int splits_of(int kt, int chunk) { return kt <= chunk ? 1 : (kt + chunk - 1) / chunk; }
+
+// The chunk: the same sums in the same order in every workgroup and in k_attend_join.
+template <int BM>
+__device__ __forceinline__ int chunk_of(const AttendArgs& g, int lane) {
+  if (g.target == 0) return INT32_MAX;
+  float total = 0.0f;
+  for (int b0 = 0; b0 < g.B; b0 += 256) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int b = b0 + 4 * lane + r;
+      if (b < g.B) {
+        const Shape x = shape_of<BM>(g, sequence(g.starts, g.lens, b, g.T));
+        total += (float)x.qt * (float)x.kt;
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  const float want = __builtin_ceilf(total * (float)g.Hk / (float)g.target);
+  return std::max(g.min_chunk, (int)fminf(want, 1073741824.0f));
+}
+
+// The sequence and range with number `idx` among a head's; with MULTI, of the row tiles that are cut into
+// several ranges, `idx` counting tiles.
+template <int BM, bool MULTI>
+__device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Work& w) {
+  const int lane = threadIdx.x & 63;
+  const int chunk = chunk_of<BM>(g, lane);
+  uint32_t before = 0, parts_before = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 256) {
+    uint32_t n[4], parts[4], mine = 0, my_parts = 0;
+    int splits[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int b = b0 + 4 * lane + r;
+      n[r] = parts[r] = 0;
+      splits[r] = 1;
+      if (b < g.B) {
+        const Shape x = shape_of<BM>(g, sequence(g.starts, g.lens, b, g.T));
+        splits[r] = splits_of(x.kt, chunk);
+        const uint32_t items = (uint32_t)x.qt * (uint32_t)splits[r];
+        parts[r] = splits[r] > 1 ? items : 0u;
+        n[r] = MULTI ? (splits[r] > 1 ? (uint32_t)x.qt : 0u) : items;
+      }
+      mine += n[r];
+      my_parts += parts[r];
+    }
+    const uint32_t incl = scan_add(mine, lane);
+    const uint32_t incl_parts = g.target ? scan_add(my_parts, lane) : 0u;
+    uint32_t at = before + incl - mine, at_parts = parts_before + incl_parts - my_parts;
+    const uint64_t hit = __ballot(idx >= at && idx - at < mine);
+    if (hit) {
+      const int who = __builtin_ctzll(hit);
+      int found = 0, found_splits = 1;
+      uint32_t rest = 0, found_parts = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (idx >= at && idx - at < n[r]) {
+          found = b0 + 4 * lane + r;
+          found_splits = splits[r];
+          rest = idx - at;
+          found_parts = at_parts;
+        }
+        at += n[r];
+        at_parts += parts[r];
+      }
+      w.b = __builtin_amdgcn_readlane(found, who);
+      w.splits = __builtin_amdgcn_readlane(found_splits, who);
+      rest = (uint32_t)__builtin_amdgcn_readlane((int)rest, who);
+      found_parts = (uint32_t)__builtin_amdgcn_readlane((int)found_parts, who);
+      w.chunk = chunk;
+      w.s = sequence(g.starts, g.lens, w.b, g.T);
+      const int qt = shape_of<BM>(g, w.s).qt;
+      // the last tile sees most: it goes first
+      const uint32_t j = MULTI ? rest : rest / (uint32_t)w.splits;
+      w.tile = qt - 1 - (int)j;
+      w.split = MULTI ? 0 : (int)(rest - j * (uint32_t)w.splits);
+      w.part = found_parts + j * (uint32_t)w.splits + (uint32_t)w.split;
+      return w.tile >= 0;
+    }
+    before += __builtin_amdgcn_readlane((int)incl, 63);
+    parts_before += __builtin_amdgcn_readlane((int)incl_parts, 63);
+  }
+  return false;
+}
+
+// What a tile's rows see: keys begin .. end - 1 in all, [all_begin, all_end) by every row; its key tiles.
+struct Sight {
+  int64_t begin, end, all_begin, all_end;
+  int kt0, kt1;
+};
+
+template <int BM>
+__device__ __forceinline__ Sight sight_of(const AttendArgs& g, const Seq& s, int tile) {
+  const int G = g.H / g.Hk;
+  const int64_t rows = (int64_t)s.n * G, last_row = std::min<int64_t>(rows, (int64_t)(tile + 1) * BM) - 1;
+  const int64_t lo = (int64_t)s.len - s.n + (int64_t)tile * BM / G, hi = (int64_t)s.len - s.n + last_row / G;   // positions
+  const int64_t held = std::min<int64_t>(s.len, g.width << g.page_shift);
+  Sight v;
+  v.end = g.causal ? std::max<int64_t>(0, std::min(held, hi + 1)) : held;
+  v.all_end = g.causal ? std::max<int64_t>(0, std::min(held, lo + 1)) : held;
+  v.begin = g.window ? std::max<int64_t>(0, lo - g.window + 1) : 0;
+  v.all_begin = g.window ? std::max<int64_t>(0, hi - g.window + 1) : 0;
+  v.kt0 = (int)std::min<int64_t>(v.begin / kKeyTile, 1 << 25);
+  v.kt1 = std::max(v.kt0, (int)((v.end + kKeyTile - 1) / kKeyTile));
+  return v;
+}
+
+// The first row of the cache (of [n_pages * Hk * page_size]) for 16 keys from `key` (a multiple of 16, on
+// one page), and whether the cache holds them: a page outside it reads page 0, masked.
+__device__ __forceinline__ int64_t rows_at(const AttendArgs& g, int b, int hk, int64_t key, bool& held) {
+  const int64_t p = std::min<int64_t>(key >> g.page_shift, g.width - 1);
+  int page = g.pages[b * g.ldp + p];
+  held = page >= 0 && page < g.n_pages && (key >> g.page_shift) < g.width;
+  page = __builtin_amdgcn_readfirstlane(held ? page : 0);
+  held = __builtin_amdgcn_readfirstlane(held);
+  return (((int64_t)page * g.Hk + hk) << g.page_shift) + (key & ((1 << g.page_shift) - 1));
+}
+
+// ---------------------------------------------------------------- numbers
+__device__ __forceinline__ float max32(float x) {   // with lane ^ 32
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max16(float x) {   // with lane ^ 16
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// 8 codes -> 8 bf16 / 4 codes -> 4 fp16, exact.
+__device__ __forceinline__ uint32_t bf16x2_of(uint32_t codes, bool high) {
+  const v2b r = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, true)
+                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, false);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes, bool high) {
+  const v2h r = high ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, true)
+                     : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, false);
+  return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
+}
+
+__device__ __forceinline__ uint4 bf16x8_of(uint2 codes) {
+  return make_uint4(bf16x2_of(codes.x, false), bf16x2_of(codes.x, true), bf16x2_of(codes.y, false), bf16x2_of(codes.y, true));
+}
+
+// Two weights in 16 bits; under bf16 they become what they were rounded to.
+template <int SCHEME>
+__device__ __forceinline__ uint32_t pack_weights(float& a, float& b) {
+  if constexpr (SCHEME == kKvBf16) {
+    const uint32_t p = gemm::pack_bf16x2(a, b);
+    a = bf16lo(p);
+    b = bf16hi(p);
+    return p;
+  } else {
+    return pack_f16x2(a, b);
   }
 }
 
-// A wave per query row: a key per lane for the scores, D / 64 values per lane for the sums.
+// 4 x 4 transposes of what four keys' loads hold: out[d] = the four keys' value d, 4 bytes (codes), or two
+// words of 16-bit values.
+__device__ __forceinline__ void transpose4(const uint32_t (&k)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(k[1], k[0], 0x05010400u), b = __builtin_amdgcn_perm(k[1], k[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(k[3], k[2], 0x05010400u), d = __builtin_amdgcn_perm(k[3], k[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+__device__ __forceinline__ uint32_t low16s(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high16s(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Whether 4 codes hold a NaN (0x7F, 0xFF), or two bf16 values a NaN or an infinity.
+__device__ __forceinline__ bool bad_codes(uint32_t c) {
+  const uint32_t m = c & 0x7F7F7F7Fu;
+  return ((m + 0x01010101u) & 0x80808080u) != 0;
+}
+__device__ __forceinline__ bool bad_bf16(uint32_t c) {
+  return (c & 0x7F80u) == 0x7F80u || (c & 0x7F800000u) == 0x7F800000u;
+}
+template <int SCHEME>
+__device__ __forceinline__ bool bad_word(uint32_t c) { return SCHEME == kKvBf16 ? bad_bf16(c) : bad_codes(c); }
+
+// A value scale as the weights take it: its logarithm and its reciprocal.
+__device__ __forceinline__ void value_scale(float vs, float& lv, float& rv) {
+  vs = vs < kSmallestValueScale ? kSmallestValueScale : vs;   // a NaN stays one
+  lv = __builtin_amdgcn_logf(vs);
+  rv = __builtin_amdgcn_rcpf(vs);
+}
+
+// The second products' operands, as 16-byte words.
+template <int SCHEME>
+__device__ __forceinline__ v4f mfma16_pv(uint4 v, uint4 w, v4f acc) {
+  if constexpr (SCHEME == kKvBf16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v), __builtin_bit_cast(v8bf, w), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, v), __builtin_bit_cast(v8h, w), acc, 0, 0, 0);
+}
+template <int SCHEME>
+__device__ __forceinline__ v16f mfma32_pv(uint4 v, uint4 w, v16f acc) {
+  if constexpr (SCHEME == kKvBf16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, v), __builtin_bit_cast(v8bf, w), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, v), __builtin_bit_cast(v8h, w), acc, 0, 0, 0);
+}
+
+// What multiplies O / l at the end, and a score before its exponential.
+template <int SCHEME>
+__device__ __forceinline__ float final_scale(const AttendArgs& g) { return SCHEME == kKvTensor ? g.v_scales[0] : 1.0f; }
+template <int SCHEME>
+__device__ __forceinline__ float score_scale(const AttendArgs& g) {
+  return g.scale * kLog2e * (SCHEME == kKvTensor ? g.k_scales[0] : 1.0f);
+}
+
+// log sum exp, natural, from m and l (l carries the weights' shift).
+template <int SCHEME>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : kLn2 * (m - weight_shift<SCHEME>() + __builtin_amdgcn_logf(l));
+}
+
+// ---------------------------------------------------------------- results
+// 8 values of a row from their sums; a row that saw nothing is zeros.
+template <int SCHEME>
+__device__ __forceinline__ void store_row(const AttendArgs& g, const Seq& s, int row, int hk, int d, const float (&acc)[8],
+                                          float m, float l, float le, float fin) {
+  const int G = g.H / g.Hk;
+  const int64_t t = s.first + row / G;
+  const int h = hk * G + row % G;
+  const float f = l == 0.0f ? 0.0f : fin / l;
+  stg16(g.out + t * g.ldot + (int64_t)h * g.ldoh + d,
+        make_uint4(gemm::pack_bf16x2(acc[0] * f, acc[1] * f), gemm::pack_bf16x2(acc[2] * f, acc[3] * f),
+                   gemm::pack_bf16x2(acc[4] * f, acc[5] * f), gemm::pack_bf16x2(acc[6] * f, acc[7] * f)));
+  if (g.lse && d == 0) g.lse[t * g.H + h] = lse_of<SCHEME>(m, SCHEME == kKvBf16 ? le : l);
+}
+
+// What the sums of a range with maximum m count for beside the highest one.  A range that saw nothing but
+// NaN has no maximum; its sums are NaN and stay.
+__device__ __forceinline__ float join_factor(float m, float l, float top) {
+  if (m == -INFINITY) return l != 0.0f ? 1.0f : 0.0f;
+  return __builtin_amdgcn_exp2f(m - top);
+}
+
+// Parts, [Hk, parts, BM, D] sums and then [Hk, parts, BM] x (m, l, l of weights as they were, unused), fp32.
+__device__ __forceinline__ float* part_sums(const AttendArgs& g, int BM, int D, int hk, uint32_t part, int row) {
+  return g.ws + (((int64_t)hk * g.parts + part) * BM + row) * D;
+}
+__device__ __forceinline__ float4* part_ml(const AttendArgs& g, int BM, int D, int hk, uint32_t part, int row) {
+  return reinterpret_cast<float4*>(g.ws + (int64_t)g.Hk * g.parts * BM * D) + ((int64_t)hk * g.parts + part) * BM + row;
+}
+
+// ---------------------------------------------------------------- few rows: keys stream past
+// 16 NQ rows per workgroup.  Four waves take 32 keys each in turn, straight from memory into the
+// registers that the 16 x 16 x 32 matrix instructions read: a lane's part of a key is D / 4 contiguous
+// values (q is read in the same order), and of a value D / 16 contiguous ones of eight keys, transposed in
+// registers.  Nothing is staged and no wave waits for another until the end, where the four (O, m, l)
+// are joined through LDS.
 template <int SCHEME, int D>
-__global__ __launch_bounds__(64) void k_attend_row(AttendArgs g) {
-  __shared__ float qs[D];
-  __shared__ float ps[64];
-  __shared__ int64_t rows[64];
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, hk = h / (g.H / g.Hk);
-  int b = -1;
-  for (int i = lane; i - lane < g.B && b < 0; i += 64) {
-    bool mine = false;
-    if (i < g.B) {
-      const Seq s = sequence(g.starts, g.lens, i, g.T);
-      mine = t >= s.first && t < s.first + s.n;
+struct StreamTile {
+  static constexpr int EB = SCHEME == kKvBf16 ? 2 : 1;       // bytes of a value
+  static constexpr int KW = D / 4 * EB / 16;                 // 16-byte loads of a lane per 16 keys
+  static constexpr int VW = D / 16 * EB / 4;                 // words of a lane per key
+  uint4 k[2][KW];
+  uint32_t v[8][VW];
+  float4 ks[2], vs[2];
+  bool held[2];
+
+  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int64_t key, int lane) {
+    const int c = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t row = rows_at(g, b, hk, key + 16 * t, held[t]);
+      const uint8_t* kp = static_cast<const uint8_t*>(g.k_codes) + row * (D * EB);
+#pragma unroll
+      for (int i = 0; i < KW; ++i) k[t][i] = ldg16(kp + c * (D * EB) + q * (D / 4 * EB) + 16 * i);
+      const uint8_t* vp = static_cast<const uint8_t*>(g.v_codes) + row * (D * EB);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        struct W { uint32_t w[VW]; };
+        const W x = *reinterpret_cast<const W*>(vp + (4 * q + i) * (D * EB) + c * (VW * 4));
+#pragma unroll
+        for (int j = 0; j < VW; ++j) v[4 * t + i][j] = x.w[j];
+      }
+      if constexpr (SCHEME == kKvRow) {
+        ks[t] = *reinterpret_cast<const float4*>(g.k_scales + row + 4 * q);
+        vs[t] = *reinterpret_cast<const float4*>(g.v_scales + row + 4 * q);
+      }
     }
-    const uint64_t m = __ballot(mine);
-    if (m) b = i - lane + __builtin_ctzll(m);
   }
-  if (b < 0) return;
-  const Seq s = sequence(g.starts, g.lens, b, g.T);
-  const int pos = s.len - s.n + (int)(t - s.first);
-  const int64_t cap = g.width << g.page_shift;
-  const int64_t end = std::min<int64_t>(cap, g.causal ? std::max(0, std::min(s.len, pos + 1)) : s.len);
-  const int64_t begin = g.window ? std::max<int64_t>(0, (int64_t)pos - g.window + 1) : 0;
-  for (int d = lane; d < D; d += 64)
-    qs[d] = __uint_as_float((uint32_t)g.q[t * g.ldqt + h * g.ldqh + d] << 16);
-  __syncthreads();
-  float m = -INFINITY, l = 0.0f, o[D / 64];
-  for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
-  for (int64_t k0 = begin; k0 < end; k0 += 64) {
-    const int64_t j = k0 + lane;
-    float sc = -INFINITY;
-    int64_t row = -1;
-    if (j < end) {
-      const int page = g.pages[b * g.ldp + (j >> g.page_shift)];
-      if (page >= 0 && page < g.n_pages) {
-        row = (((int64_t)page * g.Hk + hk) << g.page_shift) + (j & ((1 << g.page_shift) - 1));
-        const float ks = SCHEME == kKvBf16 ? 1.0f : g.k_scales[SCHEME == kKvRow ? row : 0];
-        sc = 0.0f;
-        for (int c = 0; c < D; c += 8) {
-          float f[8];
-          row8<SCHEME>(g.k_codes, row, D, c, ks, f);
-          for (int e = 0; e < 8; ++e) sc += f[e] * qs[c + e];
+};
+
+template <int SCHEME, int D, int NQ>
+__global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(AttendArgs g) {
+  constexpr int BM = 16 * NQ, JD = D / 16, EB = StreamTile<SCHEME, D>::EB, VW = StreamTile<SCHEME, D>::VW;
+  __shared__ float so[4][16][D + 4];
+  __shared__ float sm[4][16], sl[4][16], se[4][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q4 = lane >> 4;
+  const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
+  Work w;
+  if (!find_work<BM, false>(g, blockIdx.x / (uint32_t)g.Hk, w)) return;
+  const Sight v = sight_of<BM>(g, w.s, w.tile);
+  const int mine = splits_of(v.kt1 - v.kt0, w.chunk);
+  if (w.split >= mine) return;
+  const int kt_first = v.kt0 + w.split * w.chunk;   // split 0 where chunk is unbounded
+  const int kt_last = mine > 1 ? std::min(v.kt1, kt_first + w.chunk) : v.kt1;
+  const int G = g.H / g.Hk;
+  const int rows = w.s.n * G;
+
+  // this lane's rows and what they see
+  uint4 qf[NQ][D / 32];
+  int64_t row_end[NQ], row_begin[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int r = w.tile * BM + 16 * n + c;
+    const bool live = r < rows;
+    const int i = live ? r / G : 0, h = live ? hk * G + r % G : 0;
+    const uint16_t* p = g.q + (int64_t)(w.s.first + i) * g.ldqt + (int64_t)h * g.ldqh + q4 * (D / 4);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) qf[n][j] = ldg16(p + 8 * j);
+    const int64_t pos = (int64_t)w.s.len - w.s.n + i;
+    row_end[n] = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
+    row_begin[n] = g.window ? pos - g.window + 1 : 0;
+  }
+
+  const float ks0 = score_scale<SCHEME>(g);
+  v4f o[NQ][JD];
+  float m[NQ], l[NQ], le[NQ];   // le: bf16 caches, weights before their rounding
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    m[n] = -INFINITY;
+    l[n] = le[n] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < JD; ++j) o[n][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  const int64_t key_last = std::min<int64_t>((int64_t)kt_last * kKeyTile, (v.end + 31) & ~int64_t(31));
+  int64_t key = (int64_t)kt_first * kKeyTile + 32 * wave;
+  StreamTile<SCHEME, D> cur, nxt;
+  if (key < key_last) cur.load(g, w.b, hk, key, lane);
+  for (; key < key_last; key += 128) {
+    const bool more = key + 128 < key_last;
+    if (more) nxt.load(g, w.b, hk, key + 128, lane);
+    // scores of 32 keys: lane (c, q4) has row c's keys 16 t + 4 q4 + i
+    float s[NQ][8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      v4f acc[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        uint4 kf;
+        if constexpr (SCHEME == kKvBf16) kf = cur.k[t][j];
+        else kf = bf16x8_of((j & 1) ? make_uint2(cur.k[t][j >> 1].z, cur.k[t][j >> 1].w)
+                                    : make_uint2(cur.k[t][j >> 1].x, cur.k[t][j >> 1].y));
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, kf), __builtin_bit_cast(v8bf, qf[n][j]),
+                                                           acc[n], 0, 0, 0);
+      }
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[n][i];
+    }
+    float rv[8];
+    if constexpr (SCHEME == kKvRow) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float k4[4] = {cur.ks[t].x, cur.ks[t].y, cur.ks[t].z, cur.ks[t].w};
+        const float v4[4] = {cur.vs[t].x, cur.vs[t].y, cur.vs[t].z, cur.vs[t].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lv;
+          value_scale(v4[i], lv, rv[4 * t + i]);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][4 * t + i] = __builtin_fmaf(s[n][4 * t + i], k4[i] * ks0, lv);
         }
-        sc *= g.scale;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[n][i] *= ks0;
+    }
+    // Keys that some rows do not see: their scores go, and values that are not finite are taken out of the
+    // product (0 times them is not 0) and make the scores of rows that do see them NaN.
+    const bool edge = key < v.all_begin || key + 32 > v.all_end || !cur.held[0] || !cur.held[1];
+    if (edge) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bool x = false;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) x |= bad_word<SCHEME>(cur.v[i][j]);
+        bad |= (uint32_t)x << i;
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) bad |= __shfl_xor(bad, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool is_bad = (bad >> i) & 1;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) cur.v[i][j] = is_bad ? 0u : cur.v[i][j];
+        const int64_t at = key + 16 * (i >> 2) + 4 * q4 + (i & 3);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const bool seen = cur.held[i >> 2] && at < row_end[n] && at >= row_begin[n];
+          s[n][i] = !seen ? -INFINITY : is_bad ? NAN : s[n][i];
+        }
+        if constexpr (SCHEME == kKvRow) rv[i] = rv[i] == rv[i] ? rv[i] : 1.0f;   // such a scale's score is NaN where seen
       }
     }
-    const float mx = fmaxf(m, wave_max(sc));
-    const float safe = mx == -INFINITY ? 0.0f : mx;
-    const float p = row < 0 ? 0.0f : expf(sc - safe), alpha = expf(m - safe);
-    m = mx;
-    float sum = p;
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    l = l * alpha + sum;
-    ps[lane] = p;
-    rows[lane] = row;
-    __syncthreads();
-    for (int i = 0; i < D / 64; ++i) o[i] *= alpha;
-    for (int e = 0; e < 64; ++e) {
-      if (rows[e] < 0) continue;
-      const float vs = SCHEME == kKvBf16 ? 1.0f : g.v_scales[SCHEME == kKvRow ? rows[e] : 0];
-      for (int i = 0; i < D / 64; ++i) {
-        const int64_t at = rows[e] * D + 64 * i + lane;
-        float v;
-        if constexpr (SCHEME == kKvBf16) v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(g.v_codes)[at] << 16);
-        else v = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(g.v_codes)[at], 0) * vs;
-        o[i] += ps[e] * v;
+    uint4 wf[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float top = s[n][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, s[n][i]);
+      top = max32(max16(top));
+      if (__any(top > m[n] + kRise)) {
+        const float next = top > m[n] + kRise ? top : m[n];
+        const float a = next == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - next);
+        m[n] = next;
+        l[n] *= a;
+        le[n] *= a;
+#pragma unroll
+        for (int j = 0; j < JD; ++j) o[n][j] *= a;
+      }
+      const float base = m[n] == -INFINITY ? 0.0f : m[n] - weight_shift<SCHEME>();
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(s[n][i] - base);
+      if (SCHEME == kKvBf16 && g.lse)
+        le[n] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+      wf[n] = make_uint4(pack_weights<SCHEME>(x[0], x[1]), pack_weights<SCHEME>(x[2], x[3]),
+                         pack_weights<SCHEME>(x[4], x[5]), pack_weights<SCHEME>(x[6], x[7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (SCHEME == kKvRow) l[n] = __builtin_fmaf(x[i], rv[i], l[n]);
+        else l[n] += x[i];
       }
     }
+    // values: eight keys of D / 16 values each, transposed four by four
+#pragma unroll
+    for (int u = 0; u < JD / 4; ++u) {
+      uint4 vf[4];
+      if constexpr (SCHEME == kKvBf16) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = 2 * u + e;
+          vf[2 * e] = make_uint4(low16s(cur.v[0][j], cur.v[1][j]), low16s(cur.v[2][j], cur.v[3][j]),
+                                 low16s(cur.v[4][j], cur.v[5][j]), low16s(cur.v[6][j], cur.v[7][j]));
+          vf[2 * e + 1] = make_uint4(high16s(cur.v[0][j], cur.v[1][j]), high16s(cur.v[2][j], cur.v[3][j]),
+                                     high16s(cur.v[4][j], cur.v[5][j]), high16s(cur.v[6][j], cur.v[7][j]));
+        }
+      } else {
+        const uint32_t a[4] = {cur.v[0][u], cur.v[1][u], cur.v[2][u], cur.v[3][u]};
+        const uint32_t b[4] = {cur.v[4][u], cur.v[5][u], cur.v[6][u], cur.v[7][u]};
+        uint32_t ta[4], tb[4];
+        transpose4(a, ta);
+        transpose4(b, tb);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          vf[e] = make_uint4(f16x2_of(ta[e], false), f16x2_of(ta[e], true), f16x2_of(tb[e], false), f16x2_of(tb[e], true));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) o[n][4 * u + e] = mfma16_pv<SCHEME>(vf[e], wf[n], o[n][4 * u + e]);
+    }
+    if (more) cur = nxt;
+  }
+
+  // join the four waves, 16 rows at a time: lane (c, q4) holds row c's values (4 q4 + i) D / 16 + j
+  constexpr int TR = D / 8, RP = 256 / TR;   // threads per row, rows at a time
+  const int tr = threadIdx.x % TR, r0 = threadIdx.x / TR;
+  const float fin = final_scale<SCHEME>(g);
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    if (n > 0) __syncthreads();
+    l[n] = add32(add16(l[n]));
+    le[n] = add32(add16(le[n]));
+    if (q4 == 0) {
+      sm[wave][c] = m[n];
+      sl[wave][c] = l[n];
+      se[wave][c] = le[n];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < JD; j += 4)
+        *reinterpret_cast<float4*>(&so[wave][c][(4 * q4 + i) * JD + j]) =
+            make_float4(o[n][j][i], o[n][j + 1][i], o[n][j + 2][i], o[n][j + 3][i]);
     __syncthreads();
+    for (int r = r0; r < 16 && r0 < RP; r += RP) {
+      const int row = w.tile * BM + 16 * n + r;
+      if (row >= rows) break;
+      const float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = join_factor(sm[x][r], sl[x][r], top);
+        sum = __builtin_fmaf(f, sl[x][r], sum);
+        exact = __builtin_fmaf(f, se[x][r], exact);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[x][r][8 * tr + e], acc[e]);
+      }
+      if (mine == 1) {
+        store_row<SCHEME>(g, w.s, row, hk, 8 * tr, acc, top, sum, exact, fin);
+      } else if (w.part < (uint32_t)g.parts) {
+        float* p = part_sums(g, BM, D, hk, w.part, 16 * n + r) + 8 * tr;
+        *reinterpret_cast<float4*>(p) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (tr == 0) *part_ml(g, BM, D, hk, w.part, 16 * n + r) = make_float4(top, sum, exact, 0.0f);
+      }
+    }
   }
-  for (int i = 0; i < D / 64; ++i) {
-    const float y = l == 0.0f ? 0.0f : o[i] / l;
-    g.out[t * g.ldot + h * g.ldoh + 64 * i + lane] = (uint16_t)(gemm::pack_bf16x2(y, 0.0f) & 0xFFFFu);
+}
+
+// ---------------------------------------------------------------- many rows: key tiles through LDS
+// 128 rows per workgroup, 32 to a wave, 32 x 32 x 16 matrix instructions.  A tile of 64 keys (32 where a head has
+// more than 128 values) is read into registers one tile ahead, turned into 16-bit operands once for all four
+// waves on its way to LDS (values transposed, so that a fragment of both operands is one 16-byte read), and
+// double-buffered: one barrier per tile.  Two workgroups share a CU, one's softmax beside the
+// other's products.
+template <int SCHEME, int D>
+struct KeyTile {
+  static constexpr int KT = D <= 128 ? 64 : 32;
+  static constexpr int EB = SCHEME == kKvBf16 ? 2 : 1;
+  static constexpr int PK = D * EB / 16;                      // 16-byte pieces of a key
+  static constexpr int NK = (KT * PK + 255) / 256;            // pieces per thread
+  static constexpr int UV = KT / 4 * (D / 4);                 // units of 4 keys x 4 values
+  static constexpr int NV = (UV + 255) / 256;
+  static constexpr int kBytes = KT * D * 2;                   // of one operand in LDS
+
+  uint4 k[NK];
+  uint2 v[NV][4];                                             // FP8: .x alone
+  float ks, vs;
+  uint32_t held;                                              // a bit per 16 keys
+
+  static __device__ __forceinline__ int v_dq(int e) { return e % (D / 4); }
+  // Units 2 apart in a group of four keys' order lie in the two halves of a 16-byte chunk: lanes of a wave
+  // write both.
+  static __device__ __forceinline__ int v_kg(int e) {
+    const int i = e / (D / 4);
+    return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1);
   }
-  if (g.lse && lane == 0) g.lse[t * g.H + h] = l == 0.0f ? -INFINITY : m + logf(l);
+
+  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int64_t key) {
+    const int t = threadIdx.x;
+    int64_t base[KT / 16];
+    held = 0;
+#pragma unroll
+    for (int i = 0; i < KT / 16; ++i) {
+      bool h;
+      base[i] = rows_at(g, b, hk, key + 16 * i, h);
+      held |= (uint32_t)h << i;
+    }
+    auto row_of = [&](int r) {   // cache row of the tile's key r
+      int64_t x = base[0];
+#pragma unroll
+      for (int i = 1; i < KT / 16; ++i) x = (r >> 4) == i ? base[i] : x;
+      return x + (r & 15);
+    };
+#pragma unroll
+    for (int u = 0; u < NK; ++u) {
+      const int e = t + 256 * u;
+      if (KT * PK % 256 == 0 || e < KT * PK)
+        k[u] = ldg16(static_cast<const uint8_t*>(g.k_codes) + row_of(e / PK) * (D * EB) + (e % PK) * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int e = t + 256 * u;
+      if (UV % 256 == 0 || e < UV) {
+        const uint8_t* p = static_cast<const uint8_t*>(g.v_codes) + row_of(4 * v_kg(e)) * (D * EB) + v_dq(e) * (4 * EB);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (SCHEME == kKvBf16) v[u][i] = *reinterpret_cast<const uint2*>(p + i * (D * EB));
+          else v[u][i].x = *reinterpret_cast<const uint32_t*>(p + i * (D * EB));
+        }
+      }
+    }
+    if constexpr (SCHEME == kKvRow) {
+      if (t < KT) {
+        const int64_t r = row_of(t);
+        ks = g.k_scales[r];
+        vs = g.v_scales[r];
+      }
+    }
+  }
+
+  // Where 16-byte chunk c (8 values) of key r lies, and 4 keys x 1 value of the transposed values: chosen so that
+  // 16 lanes that read one chunk of consecutive rows meet all 64 banks.
+  static __device__ __forceinline__ int k_at(int r, int c) {
+    return r * (D * 2) + ((D % 128 == 0 ? c ^ (r & 15) : c ^ ((r >> 1) & 7)) << 4);
+  }
+  static __device__ __forceinline__ int v_row(int d) { return d * (KT * 2); }
+  static __device__ __forceinline__ int v_swizzle(int d) {
+    return KT == 64 ? ((d >> 1) & 7) ^ ((d >> 4) & 1) : (d >> 2) & 3;
+  }
+  static __device__ __forceinline__ int v_at(int d, int kg) {
+    return v_row(d) + (((2 * (kg >> 2) + (kg & 1)) ^ v_swizzle(d)) << 4) + ((kg >> 1) & 1) * 8;
+  }
+
+  // edge: some row does not see every key of the tile.  Values that are not finite are then left out, and their
+  // key is marked with the tile's number.
+  __device__ __forceinline__ void store(uint8_t* kl, uint8_t* vl, float* params, int* marks, bool edge, int number,
+                                        float ks0) {
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < NK; ++u) {
+      const int e = t + 256 * u;
+      if (KT * PK % 256 == 0 || e < KT * PK) {
+        const int r = e / PK, c = e % PK;
+        if constexpr (SCHEME == kKvBf16) {
+          stg16(kl + k_at(r, c), k[u]);
+        } else {
+          stg16(kl + k_at(r, 2 * c), bf16x8_of(make_uint2(k[u].x, k[u].y)));
+          stg16(kl + k_at(r, 2 * c + 1), bf16x8_of(make_uint2(k[u].z, k[u].w)));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int e = t + 256 * u;
+      if (UV % 256 == 0 || e < UV) {
+        const int d0 = 4 * v_dq(e), kg = v_kg(e);
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bool bad = bad_word<SCHEME>(v[u][i].x);
+            if constexpr (SCHEME == kKvBf16) bad |= bad_word<SCHEME>(v[u][i].y);
+            if (bad) {
+              v[u][i] = make_uint2(0u, 0u);
+              marks[4 * kg + i] = number;
+            }
+          }
+        }
+        uint2 out[4];
+        if constexpr (SCHEME == kKvBf16) {
+          out[0] = make_uint2(low16s(v[u][0].x, v[u][1].x), low16s(v[u][2].x, v[u][3].x));
+          out[1] = make_uint2(high16s(v[u][0].x, v[u][1].x), high16s(v[u][2].x, v[u][3].x));
+          out[2] = make_uint2(low16s(v[u][0].y, v[u][1].y), low16s(v[u][2].y, v[u][3].y));
+          out[3] = make_uint2(high16s(v[u][0].y, v[u][1].y), high16s(v[u][2].y, v[u][3].y));
+        } else {
+          const uint32_t a[4] = {v[u][0].x, v[u][1].x, v[u][2].x, v[u][3].x};
+          uint32_t ta[4];
+          transpose4(a, ta);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = make_uint2(f16x2_of(ta[i], false), f16x2_of(ta[i], true));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) stg8(vl + v_at(d0 + i, kg), out[i]);
+      }
+    }
+    if constexpr (SCHEME == kKvRow) {
+      if (t < KT) {
+        float lv, rv;
+        value_scale(vs, lv, rv);
+        params[t] = ks * ks0;
+        params[KT + t] = lv;
+        params[2 * KT + t] = rv == rv ? rv : 1.0f;   // such a scale's score is NaN where seen
+      }
+    }
+  }
+};
+
+template <int SCHEME, int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArgs g) {
+  typedef KeyTile<SCHEME, D> Tile;
+  constexpr int BM = 128, KT = Tile::KT, NB = KT / 32, ND = D / 32;
+  __shared__ __align__(16) uint8_t lds_k[2][Tile::kBytes];
+  __shared__ __align__(16) uint8_t lds_v[2][Tile::kBytes];
+  __shared__ __align__(16) float params[2][SCHEME == kKvRow ? 3 * KT : 4];
+  __shared__ __align__(16) int marks[2][KT];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, h2 = lane >> 5;
+  const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
+  Work w;
+  if (!find_work<BM, false>(g, blockIdx.x / (uint32_t)g.Hk, w)) return;
+  const Sight v = sight_of<BM>(g, w.s, w.tile);
+  const int mine = splits_of(v.kt1 - v.kt0, w.chunk);
+  if (w.split >= mine) return;
+  const int kt_first = v.kt0 + w.split * w.chunk;
+  const int kt_last = mine > 1 ? std::min(v.kt1, kt_first + w.chunk) : v.kt1;
+  const int G = g.H / g.Hk;
+  const int rows = w.s.n * G;
+
+  const int row = w.tile * BM + 32 * wave + c;
+  const bool live = row < rows;
+  const bool wave_live = w.tile * BM + 32 * wave < rows;
+  const int i = live ? row / G : 0, h = live ? hk * G + row % G : 0;
+  uint4 qf[D / 16];
+  {
+    const uint16_t* p = g.q + (int64_t)(w.s.first + i) * g.ldqt + (int64_t)h * g.ldqh + 8 * h2;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) qf[j] = ldg16(p + 16 * j);
+  }
+  const int64_t pos = (int64_t)w.s.len - w.s.n + i;
+  const int64_t row_end = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
+  const int64_t row_begin = g.window ? pos - g.window + 1 : 0;
+  // the last key that any row of this wave sees, and the first
+  const int last = std::min(rows, w.tile * BM + 32 * wave + 32) - 1;
+  const int64_t wave_end = g.causal ? std::min(v.end, (int64_t)w.s.len - w.s.n + last / G + 1) : v.end;
+  const int64_t wave_begin =
+      g.window ? (int64_t)w.s.len - w.s.n + (w.tile * BM + 32 * wave) / G - g.window + 1 : 0;
+
+  const float ks0 = score_scale<SCHEME>(g);
+  v16f o[ND];
+#pragma unroll
+  for (int j = 0; j < ND; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
+  float m = -INFINITY, l = 0.0f, le = 0.0f;   // le: bf16 caches, weights before their rounding
+
+  const int64_t key_first = (int64_t)kt_first * kKeyTile;
+  const int64_t key_last = std::min<int64_t>((int64_t)kt_last * kKeyTile, (v.end + KT - 1) / KT * KT);
+  const int tiles = key_last > key_first ? (int)((key_last - key_first) / KT) : 0;
+  auto is_edge = [&](int64_t key, uint32_t held) {
+    return key < v.all_begin || key + KT > v.all_end || held != (1u << (KT / 16)) - 1;
+  };
+  if (threadIdx.x < KT) marks[0][threadIdx.x] = marks[1][threadIdx.x] = -1;
+  __syncthreads();
+  Tile next;
+  uint32_t held = 0;
+  if (tiles > 0) {
+    next.load(g, w.b, hk, key_first);
+    held = next.held;
+    next.store(lds_k[0], lds_v[0], params[0], marks[0], is_edge(key_first, held), 0, ks0);
+    if (tiles > 1) next.load(g, w.b, hk, key_first + KT);
+  }
+  const int k_lane = Tile::k_at(c, h2);            // key c's chunk h2; chunk 2 j + h2 is an exclusive or away
+  constexpr int kGroup = D % 128 == 0 ? 8 : 4;     // fragments whose chunks the swizzle permutes among themselves
+  for (int x = 0; x < tiles; ++x) {
+    __syncthreads();
+    const int buf = x & 1;
+    const int64_t key = key_first + (int64_t)x * KT;
+    const bool edge = is_edge(key, held);
+    const uint32_t held_now = held;
+    if (x + 1 < tiles) {
+      held = next.held;
+      next.store(lds_k[buf ^ 1], lds_v[buf ^ 1], params[buf ^ 1], marks[buf ^ 1], is_edge(key + KT, held), x + 1, ks0);
+      if (x + 2 < tiles) next.load(g, w.b, hk, key + 2 * KT);
+    }
+    if (!wave_live || key >= wave_end || key + KT <= wave_begin) continue;
+    const uint8_t* kl = lds_k[buf];
+    const uint8_t* vl = lds_v[buf];
+    v16f s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const uint4 kf = ldg16(kl + b * 32 * (D * 2) + j / kGroup * (32 * kGroup) + (k_lane ^ (j % kGroup << 5)));
+        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, kf), __builtin_bit_cast(v8bf, qf[j]), s[b],
+                                                       0, 0, 0);
+      }
+    }
+    // lane (c, h2) has row c's keys 32 b + 8 (r / 4) + 4 h2 + r % 4
+    const float* pr = params[buf];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if constexpr (SCHEME == kKvRow) {
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(pr + 32 * b + 2 * r + 4 * h2);
+          const float4 l4 = *reinterpret_cast<const float4*>(pr + KT + 32 * b + 2 * r + 4 * h2);
+          s[b][r] = __builtin_fmaf(s[b][r], k4.x, l4.x);
+          s[b][r + 1] = __builtin_fmaf(s[b][r + 1], k4.y, l4.y);
+          s[b][r + 2] = __builtin_fmaf(s[b][r + 2], k4.z, l4.z);
+          s[b][r + 3] = __builtin_fmaf(s[b][r + 3], k4.w, l4.w);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[b][r] *= ks0;
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int kk = 32 * b + 8 * (r >> 2) + 4 * h2 + (r & 3);
+          const bool seen = ((held_now >> (2 * b + (r >> 3))) & 1) && key + kk < row_end && key + kk >= row_begin;
+          s[b][r] = !seen ? -INFINITY : marks[buf][kk] == x ? NAN : s[b][r];
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+    top = max32(top);
+    if (__any(top > m + kRise)) {
+      const float nm = top > m + kRise ? top : m;
+      const float a = nm == m ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+      m = nm;
+      l *= a;
+      le *= a;
+#pragma unroll
+      for (int j = 0; j < ND; ++j) o[j] *= a;
+    }
+    const float base = m == -INFINITY ? 0.0f : m - weight_shift<SCHEME>();
+    uint4 wf[2 * NB];
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[b][r] = __builtin_amdgcn_exp2f(s[b][r] - base);
+      if (SCHEME == kKvBf16 && g.lse) {
+        float e = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) e += s[b][r];
+        le += e;
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a0 = s[b][8 * f + 2 * e], a1 = s[b][8 * f + 2 * e + 1];
+          p[e] = pack_weights<SCHEME>(a0, a1);
+          if constexpr (SCHEME == kKvBf16) {
+            s[b][8 * f + 2 * e] = a0;
+            s[b][8 * f + 2 * e + 1] = a1;
+          }
+        }
+        wf[2 * b + f] = make_uint4(p[0], p[1], p[2], p[3]);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        if constexpr (SCHEME == kKvRow) {
+          const float4 r4 = *reinterpret_cast<const float4*>(pr + 2 * KT + 32 * b + 2 * r + 4 * h2);
+          sum[0] = __builtin_fmaf(s[b][r], r4.x, sum[0]);
+          sum[1] = __builtin_fmaf(s[b][r + 1], r4.y, sum[1]);
+          sum[2] = __builtin_fmaf(s[b][r + 2], r4.z, sum[2]);
+          sum[3] = __builtin_fmaf(s[b][r + 3], r4.w, sum[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] += s[b][r + e];
+        }
+      }
+    }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+    for (int f = 0; f < 2 * NB; ++f)
+#pragma unroll
+      for (int j = 0; j < ND; ++j) {
+        const int d = 32 * j + c;
+        const uint4 vf = ldg16(vl + Tile::v_row(d) + (((2 * f + h2) ^ Tile::v_swizzle(d)) << 4));
+        o[j] = mfma32_pv<SCHEME>(vf, wf[f], o[j]);
+      }
+  }
+
+  // lane (c, h2) has row c's values 32 j + 8 (r / 4) + 4 h2 + r % 4
+  l = add32(l);
+  le = add32(le);
+  if (mine > 1) {
+    if (!live || w.part >= (uint32_t)g.parts) return;
+    const int r_in = 32 * wave + c;
+    float* p = part_sums(g, BM, D, hk, w.part, r_in);
+#pragma unroll
+    for (int j = 0; j < ND; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4*>(p + 32 * j + 2 * r + 4 * h2) = make_float4(o[j][r], o[j][r + 1], o[j][r + 2], o[j][r + 3]);
+    if (h2 == 0) *part_ml(g, BM, D, hk, w.part, r_in) = make_float4(m, l, le, 0.0f);
+    return;
+  }
+  const float f = l == 0.0f ? 0.0f : final_scale<SCHEME>(g) / l;
+  const int64_t t = w.s.first + i;
+  uint16_t* out = g.out + t * g.ldot + (int64_t)h * g.ldoh;
+#pragma unroll
+  for (int j = 0; j < ND; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; r += 8) {
+      // lanes c and c + 32 exchange, so that each has 8 consecutive values
+      const auto lo = __builtin_amdgcn_permlane32_swap(gemm::pack_bf16x2(o[j][r] * f, o[j][r + 1] * f),
+                                                       gemm::pack_bf16x2(o[j][r + 4] * f, o[j][r + 5] * f), false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(gemm::pack_bf16x2(o[j][r + 2] * f, o[j][r + 3] * f),
+                                                       gemm::pack_bf16x2(o[j][r + 6] * f, o[j][r + 7] * f), false, false);
+      if (live) stg16(out + 32 * j + 2 * r + 8 * h2, make_uint4(lo[0], hi[0], lo[1], hi[1]));
+    }
+  if (g.lse && live && h2 == 0) g.lse[t * g.H + h] = lse_of<SCHEME>(m, SCHEME == kKvBf16 ? le : l);
+}
+
+// ---------------------------------------------------------------- join
+// The rows of a tile whose keys were cut into several ranges: the ranges' sums, each at its own maximum.
+template <int SCHEME, int BM>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
+  const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
+  Work w;
+  if (!find_work<BM, true>(g, blockIdx.x / (uint32_t)g.Hk, w)) return;
+  const Sight v = sight_of<BM>(g, w.s, w.tile);
+  const int mine = splits_of(v.kt1 - v.kt0, w.chunk);
+  if (mine < 2 || (uint64_t)w.part + (uint64_t)mine > (uint64_t)g.parts) return;
+  const int G = g.H / g.Hk, rows = w.s.n * G, tr = g.D / 8, rp = 256 / tr;
+  const int d = (int)(threadIdx.x % (uint32_t)tr) * 8, r0 = (int)(threadIdx.x / (uint32_t)tr);
+  if (r0 >= rp) return;
+  const float fin = final_scale<SCHEME>(g);
+  for (int r = r0; r < BM; r += rp) {
+    const int row = w.tile * BM + r;
+    if (row >= rows) return;
+    float top = -INFINITY;
+    for (int x = 0; x < mine; ++x) top = fmaxf(top, part_ml(g, BM, g.D, hk, w.part + x, r)->x);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
+    for (int x = 0; x < mine; ++x) {
+      const float4 ml = *part_ml(g, BM, g.D, hk, w.part + x, r);
+      const float f = join_factor(ml.x, ml.y, top);
+      const float* p = part_sums(g, BM, g.D, hk, w.part + x, r) + d;
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      sum = __builtin_fmaf(f, ml.y, sum);
+      exact = __builtin_fmaf(f, ml.z, exact);
+      acc[0] = __builtin_fmaf(f, a.x, acc[0]);
+      acc[1] = __builtin_fmaf(f, a.y, acc[1]);
+      acc[2] = __builtin_fmaf(f, a.z, acc[2]);
+      acc[3] = __builtin_fmaf(f, a.w, acc[3]);
+      acc[4] = __builtin_fmaf(f, b.x, acc[4]);
+      acc[5] = __builtin_fmaf(f, b.y, acc[5]);
+      acc[6] = __builtin_fmaf(f, b.z, acc[6]);
+      acc[7] = __builtin_fmaf(f, b.w, acc[7]);
+    }
+    store_row<SCHEME>(g, w.s, row, hk, d, acc, top, sum, exact, fin);
+  }
+}
+
+// ---------------------------------------------------------------- choice and launch
+// Rows per tile by the mean rows of a sequence's head; at most `target` ranges where contexts are worth
+// cutting.
+struct Plan {
+  int bm;
+  int target, min_chunk;
+  int64_t tiles, parts;   // bounds, per head of the cache
+};
+
+Plan plan_of(const AttendArgs& g) {
+  const int64_t rows = g.T * (g.H / g.Hk), seqs = std::max<int64_t>(1, std::min<int64_t>(g.B, g.T));
+  const int64_t mean = (rows + seqs - 1) / seqs;
+  Plan p;
+  p.bm = mean <= 16 ? 16 : mean <= 32 ? 32 : 128;
+  p.tiles = rows / p.bm + seqs;
+  p.target = p.bm == 128 ? 512 : 1024;
+  p.min_chunk = p.bm == 128 ? 16 : 4;
+  const int64_t key_tiles = ((g.width << g.page_shift) + kKeyTile - 1) / kKeyTile;
+  p.parts = 0;
+  if (key_tiles <= p.min_chunk) p.target = 0;
+  else
+    // a tile of kt > chunk key tiles has at most kt / chunk + 1 < 2 kt / chunk ranges, and chunk >= total Hk / target
+    p.parts = std::min<int64_t>(2 * ((int64_t)p.target / g.Hk + 1) + 32, p.tiles * ((key_tiles + p.min_chunk - 1) / p.min_chunk));
+  return p;
+}
+
+template <int SCHEME, int D>
+hipError_t attend_with(AttendArgs& g, const Plan& p, hipStream_t st) {
+  const dim3 grid((unsigned)((p.tiles + p.parts) * g.Hk));
+  if (p.bm == 16) hipLaunchKernelGGL((k_attend_stream<SCHEME, D, 1>), grid, dim3(256), 0, st, g);
+  else if (p.bm == 32) hipLaunchKernelGGL((k_attend_stream<SCHEME, D, 2>), grid, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((k_attend_tile<SCHEME, D>), grid, dim3(256), 0, st, g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.target == 0) return e;
+  const dim3 joins((unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk));
+  if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16>), joins, dim3(256), 0, st, g);
+  else if (p.bm == 32) hipLaunchKernelGGL((k_attend_join<SCHEME, 32>), joins, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((k_attend_join<SCHEME, 128>), joins, dim3(256), 0, st, g);
+  return hipGetLastError();
 }
 
 template <int SCHEME>
-hipError_t attend_as(const AttendArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)g.T, (unsigned)g.H);
-  if (g.D == 64) hipLaunchKernelGGL((k_attend_row<SCHEME, 64>), grid, dim3(64), 0, st, g);
-  else if (g.D == 128) hipLaunchKernelGGL((k_attend_row<SCHEME, 128>), grid, dim3(64), 0, st, g);
-  else if (g.D == 192) hipLaunchKernelGGL((k_attend_row<SCHEME, 192>), grid, dim3(64), 0, st, g);
-  else hipLaunchKernelGGL((k_attend_row<SCHEME, 256>), grid, dim3(64), 0, st, g);
-  return hipGetLastError();
+hipError_t attend_as(AttendArgs& g, const Plan& p, hipStream_t st) {
+  if (g.D == 64) return attend_with<SCHEME, 64>(g, p, st);
+  if (g.D == 128) return attend_with<SCHEME, 128>(g, p, st);
+  return g.D == 192 ? attend_with<SCHEME, 192>(g, p, st) : attend_with<SCHEME, 256>(g, p, st);
 }
 
 }  // namespace
 
-bool kv_attention_fits(const AttendArgs& g) { return g.T < (int64_t(1) << 25) && g.T * g.H < (int64_t(1) << 24); }   // threads
-
-size_t kv_attention_ws_bytes(const AttendArgs&) { return 0; }
-
-hipError_t launch_kv_attention(int scheme, AttendArgs g, hipStream_t st) {
-  if (scheme == kKvBf16) return attend_as<kKvBf16>(g, st);
-  return scheme == kKvTensor ? attend_as<kKvTensor>(g, st) : attend_as<kKvRow>(g, st);
+bool kv_attention_fits(const AttendArgs& g) {
+  const Plan p = plan_of(g);
+  return (p.tiles + p.parts) * g.Hk < (int64_t(1) << 24);   // a launch has at most 2^32 - 1 threads
 }
 
-const char* kv_attention_kernel_name(const AttendArgs&) { return "k_attend_row"; }
+size_t kv_attention_ws_bytes(const AttendArgs& g) {
+  const Plan p = plan_of(g);
+  return (size_t)p.parts * g.Hk * p.bm * (g.D + 4) * 4;
+}
+
+hipError_t launch_kv_attention(int scheme, AttendArgs g, hipStream_t st) {
+  const Plan p = plan_of(g);
+  g.target = p.target;
+  g.min_chunk = p.min_chunk;
+  g.parts = (int)p.parts;
+  if (scheme == kKvBf16) return attend_as<kKvBf16>(g, p, st);
+  return scheme == kKvTensor ? attend_as<kKvTensor>(g, p, st) : attend_as<kKvRow>(g, p, st);
+}
+
+const char* kv_attention_kernel_name(const AttendArgs& g) {
+  const Plan p = plan_of(g);
+  if (p.target) return p.bm == 16 ? "k_attend_stream<16>+k_attend_join" : p.bm == 32 ? "k_attend_stream<32>+k_attend_join" : "k_attend_tile+k_attend_join";
+  return p.bm == 16 ? "k_attend_stream<16>" : p.bm == 32 ? "k_attend_stream<32>" : "k_attend_tile";
+}
 
 }  // namespace pql

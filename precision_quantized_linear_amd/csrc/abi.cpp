@@ -1451,7 +1451,7 @@ static pql_status kv_attention_impl(int scheme, const void* q, int64_t ldqt, int
   g.pages = pages;
   g.ldp = ldp;
   g.causal = causal != 0;
-  g.window = (int)(window > kInt31 ? 0 : window);   // a window past any length hides nothing
+  g.window = (int)(window > (int64_t(1) << 30) ? 0 : window);   // hides nothing: no key is past 2^30
   g.scale = scale;
   g.out = static_cast<uint16_t*>(out);
   g.ldot = ldot;

@@ -52,97 +52,113 @@ constexpr int kKeyTile = 64;
 
 struct Work {
   Seq s;
-  int b, tile, split, splits, chunk;   // splits: of the sequence; a tile may need fewer
-  uint32_t part;                       // place of its range among those of a head
+  int b, tile, split, chunk;
+  uint32_t part;   // place of its range among those of a head
 };
 
-struct Shape {
-  int rows, qt, kt;   // rows of one head, row tiles, key tiles that any of them sees
-};
-
-template <int BM>
-__device__ __forceinline__ Shape shape_of(const AttendArgs& g, const Seq& s) {
-  Shape r;
-  const int64_t rows = (int64_t)s.n * (g.H / g.Hk);   // below 2^31: T H is
-  r.rows = (int)rows;
-  r.qt = (int)((rows + BM - 1) / BM);
-  const int64_t end = std::min<int64_t>(s.len, g.width << g.page_shift);
-  const int64_t begin = g.window ? std::max<int64_t>(0, (int64_t)s.len - s.n - g.window + 1) : 0;
-  const int64_t kt = (end + kKeyTile - 1) / kKeyTile - begin / kKeyTile;
-  r.kt = (int)std::max<int64_t>(0, kt);
-  return r;
-}
-
-__device__ __forceinline__ uint32_t scan_add(uint32_t v, int lane) {   // inclusive, over the wave
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// Sums over the wave by data-parallel moves: within rows of 16, then row to row.
+__device__ __forceinline__ uint32_t scan_add(uint32_t v) {   // inclusive
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // from 1, 2, 4, 8 lanes below
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, true);   // row 0's and 2's last lane to the next row
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, true);   // row 1's last lane to rows 2 and 3
   return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#define PQL_ADD_DPP(ctrl, rows) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xF, true))
+  PQL_ADD_DPP(0x111, 0xF);
+  PQL_ADD_DPP(0x112, 0xF);
+  PQL_ADD_DPP(0x114, 0xF);
+  PQL_ADD_DPP(0x118, 0xF);
+  PQL_ADD_DPP(0x142, 0xA);
+  PQL_ADD_DPP(0x143, 0xC);
+#undef PQL_ADD_DPP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 __device__ __forceinline__ int splits_of(int kt, int chunk) { return kt <= chunk ? 1 : (kt + chunk - 1) / chunk; }
 
-// The chunk: the same sums in the same order in every workgroup and in k_attend_join.
+// Four consecutive sequences of a lane: their rows, row tiles and the key tiles that any of their rows sees.
+// Row counts stay below 2^28 (T H D <= 2^34), key tiles below 2^25.
 template <int BM>
-__device__ __forceinline__ int chunk_of(const AttendArgs& g, int lane) {
-  if (g.target == 0) return INT32_MAX;
-  float total = 0.0f;
-  for (int b0 = 0; b0 < g.B; b0 += 256) {
+struct Shapes {
+  Seq s[4];
+  int qt[4], kt[4];
+  __device__ __forceinline__ void load(const AttendArgs& g, int b0) {
+    const int lane = threadIdx.x & 63, G = g.H / g.Hk;
+    const int64_t cap = g.width << g.page_shift;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int b = b0 + 4 * lane + r;
-      if (b < g.B) {
-        const Shape x = shape_of<BM>(g, sequence(g.starts, g.lens, b, g.T));
-        total += (float)x.qt * (float)x.kt;
-      }
+      s[r] = Seq{0, 0, 0};
+      if (b < g.B) s[r] = sequence(g.starts, g.lens, b, g.T);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      qt[r] = (s[r].n * G + BM - 1) / BM;
+      const int end = (int)std::min<int64_t>(s[r].len, cap);
+      const int begin = g.window ? std::max(0, s[r].len - s[r].n - g.window + 1) : 0;   // window <= 2^30
+      kt[r] = std::max(0, (end + kKeyTile - 1) / kKeyTile - begin / kKeyTile);
     }
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-  const float want = __builtin_ceilf(total * (float)g.Hk / (float)g.target);
-  return std::max(g.min_chunk, (int)fminf(want, 1073741824.0f));
-}
+  __device__ __forceinline__ float work() const {
+    return ((float)qt[0] * (float)kt[0] + (float)qt[1] * (float)kt[1]) +
+           ((float)qt[2] * (float)kt[2] + (float)qt[3] * (float)kt[3]);
+  }
+};
 
-// The sequence and range with number `idx` among a head's; with MULTI, of the row tiles that are cut into
-// several ranges, `idx` counting tiles.
+// The range with number `idx` among a head's; with MULTI, of the row tiles of sequences that are cut, the
+// tile with number idx.  The chunk comes out of the same sums in the same order in every workgroup
+// and in k_attend_join.
 template <int BM, bool MULTI>
 __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Work& w) {
   const int lane = threadIdx.x & 63;
-  const int chunk = chunk_of<BM>(g, lane);
+  Shapes<BM> x;
+  x.load(g, 0);
+  int chunk = INT32_MAX;
+  if (g.target) {
+    float total = x.work();
+    for (int b0 = 256; b0 < g.B; b0 += 256) {
+      x.load(g, b0);
+      total += x.work();
+    }
+    if (g.B > 256) x.load(g, 0);
+    const float want = __builtin_ceilf(wave_sum(total) * (float)g.Hk / (float)g.target);
+    chunk = std::max(g.min_chunk, (int)fminf(want, 1073741824.0f));
+    chunk = __builtin_amdgcn_readfirstlane(chunk);
+  }
   uint32_t before = 0, parts_before = 0;
   for (int b0 = 0; b0 < g.B; b0 += 256) {
+    if (b0) x.load(g, b0);
     uint32_t n[4], parts[4], mine = 0, my_parts = 0;
     int splits[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int b = b0 + 4 * lane + r;
-      n[r] = parts[r] = 0;
-      splits[r] = 1;
-      if (b < g.B) {
-        const Shape x = shape_of<BM>(g, sequence(g.starts, g.lens, b, g.T));
-        splits[r] = splits_of(x.kt, chunk);
-        const uint32_t items = (uint32_t)x.qt * (uint32_t)splits[r];
-        parts[r] = splits[r] > 1 ? items : 0u;
-        n[r] = MULTI ? (splits[r] > 1 ? (uint32_t)x.qt : 0u) : items;
-      }
+      splits[r] = splits_of(x.kt[r], chunk);
+      const uint32_t items = (uint32_t)x.qt[r] * (uint32_t)splits[r];
+      parts[r] = splits[r] > 1 ? items : 0u;
+      n[r] = MULTI ? (splits[r] > 1 ? (uint32_t)x.qt[r] : 0u) : items;
       mine += n[r];
       my_parts += parts[r];
     }
-    const uint32_t incl = scan_add(mine, lane);
-    const uint32_t incl_parts = g.target ? scan_add(my_parts, lane) : 0u;
+    const uint32_t incl = scan_add(mine), incl_parts = scan_add(my_parts);
     uint32_t at = before + incl - mine, at_parts = parts_before + incl_parts - my_parts;
     const uint64_t hit = __ballot(idx >= at && idx - at < mine);
     if (hit) {
       const int who = __builtin_ctzll(hit);
-      int found = 0, found_splits = 1;
+      int found = 0, found_splits = 1, found_qt = 0;
+      Seq found_s{0, 0, 0};
       uint32_t rest = 0, found_parts = 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (idx >= at && idx - at < n[r]) {
           found = b0 + 4 * lane + r;
           found_splits = splits[r];
+          found_qt = x.qt[r];
+          found_s = x.s[r];
           rest = idx - at;
           found_parts = at_parts;
         }
@@ -150,53 +166,54 @@ __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Wor
         at_parts += parts[r];
       }
       w.b = __builtin_amdgcn_readlane(found, who);
-      w.splits = __builtin_amdgcn_readlane(found_splits, who);
+      w.s = Seq{__builtin_amdgcn_readlane(found_s.first, who), __builtin_amdgcn_readlane(found_s.n, who),
+                __builtin_amdgcn_readlane(found_s.len, who)};
+      const uint32_t splits_b = (uint32_t)__builtin_amdgcn_readlane(found_splits, who);
+      const int qt = __builtin_amdgcn_readlane(found_qt, who);
       rest = (uint32_t)__builtin_amdgcn_readlane((int)rest, who);
       found_parts = (uint32_t)__builtin_amdgcn_readlane((int)found_parts, who);
       w.chunk = chunk;
-      w.s = sequence(g.starts, g.lens, w.b, g.T);
-      const int qt = shape_of<BM>(g, w.s).qt;
       // the last tile sees most: it goes first
-      const uint32_t j = MULTI ? rest : rest / (uint32_t)w.splits;
+      const uint32_t j = MULTI || splits_b == 1 ? rest : rest / splits_b;
       w.tile = qt - 1 - (int)j;
-      w.split = MULTI ? 0 : (int)(rest - j * (uint32_t)w.splits);
-      w.part = found_parts + j * (uint32_t)w.splits + (uint32_t)w.split;
+      w.split = MULTI ? 0 : (int)(rest - j * splits_b);
+      w.part = found_parts + j * splits_b + (uint32_t)w.split;
       return w.tile >= 0;
     }
-    before += __builtin_amdgcn_readlane((int)incl, 63);
-    parts_before += __builtin_amdgcn_readlane((int)incl_parts, 63);
+    before += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+    parts_before += (uint32_t)__builtin_amdgcn_readlane((int)incl_parts, 63);
   }
   return false;
 }
 
-// What a tile's rows see: keys begin .. end - 1 in all, [all_begin, all_end) by every row; its key tiles.
+// What a tile's rows see: keys begin .. end - 1 in all, all_begin .. all_end - 1 by every row; its key tiles.
 struct Sight {
-  int64_t begin, end, all_begin, all_end;
+  int begin, end, all_begin, all_end;
   int kt0, kt1;
 };
 
 template <int BM>
 __device__ __forceinline__ Sight sight_of(const AttendArgs& g, const Seq& s, int tile) {
   const int G = g.H / g.Hk;
-  const int64_t rows = (int64_t)s.n * G, last_row = std::min<int64_t>(rows, (int64_t)(tile + 1) * BM) - 1;
-  const int64_t lo = (int64_t)s.len - s.n + (int64_t)tile * BM / G, hi = (int64_t)s.len - s.n + last_row / G;   // positions
-  const int64_t held = std::min<int64_t>(s.len, g.width << g.page_shift);
+  const int rows = s.n * G, last_row = std::min(rows, (tile + 1) * BM) - 1;
+  const int lo = s.len - s.n + tile * BM / G, hi = s.len - s.n + last_row / G;   // positions of the first and last row
+  const int held = (int)std::min<int64_t>(s.len, g.width << g.page_shift);
   Sight v;
-  v.end = g.causal ? std::max<int64_t>(0, std::min(held, hi + 1)) : held;
-  v.all_end = g.causal ? std::max<int64_t>(0, std::min(held, lo + 1)) : held;
-  v.begin = g.window ? std::max<int64_t>(0, lo - g.window + 1) : 0;
-  v.all_begin = g.window ? std::max<int64_t>(0, hi - g.window + 1) : 0;
-  v.kt0 = (int)std::min<int64_t>(v.begin / kKeyTile, 1 << 25);
-  v.kt1 = std::max(v.kt0, (int)((v.end + kKeyTile - 1) / kKeyTile));
+  v.end = g.causal ? std::max(0, std::min(held, hi + 1)) : held;
+  v.all_end = g.causal ? std::max(0, std::min(held, lo + 1)) : held;
+  v.begin = g.window ? std::max(0, lo - g.window + 1) : 0;
+  v.all_begin = g.window ? std::max(0, hi - g.window + 1) : 0;
+  v.kt0 = std::min(v.begin, v.end) / kKeyTile;   // a window past the end (a length past the pages) sees none
+  v.kt1 = std::max(v.kt0, (v.end + kKeyTile - 1) / kKeyTile);
   return v;
 }
 
 // The first row of the cache (of [n_pages * Hk * page_size]) for 16 keys from `key` (a multiple of 16, on
 // one page), and whether the cache holds them: a page outside it reads page 0, masked.
-__device__ __forceinline__ int64_t rows_at(const AttendArgs& g, int b, int hk, int64_t key, bool& held) {
-  const int64_t p = std::min<int64_t>(key >> g.page_shift, g.width - 1);
-  int page = g.pages[b * g.ldp + p];
-  held = page >= 0 && page < g.n_pages && (key >> g.page_shift) < g.width;
+__device__ __forceinline__ int64_t rows_at(const AttendArgs& g, int b, int hk, int key, bool& held) {
+  const int p = key >> g.page_shift, last = (int)g.width - 1;
+  int page = g.pages[b * g.ldp + std::min(p, last)];
+  held = page >= 0 && page < g.n_pages && p <= last;
   page = __builtin_amdgcn_readfirstlane(held ? page : 0);
   held = __builtin_amdgcn_readfirstlane(held);
   return (((int64_t)page * g.Hk + hk) << g.page_shift) + (key & ((1 << g.page_shift) - 1));
@@ -357,35 +374,54 @@ struct StreamTile {
   uint4 k[2][KW];
   uint32_t v[8][VW];
   float4 ks[2], vs[2];
-  bool held[2];
+  int64_t row[2];
+  bool held[2], next_held[2];
 
-  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int64_t key, int lane) {
+  __device__ __forceinline__ void find(const AttendArgs& g, int b, int hk, int key) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) row[t] = rows_at(g, b, hk, key + 16 * t, next_held[t]);
+  }
+  __device__ __forceinline__ void load_k(const AttendArgs& g, int lane) {
     const int c = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t row = rows_at(g, b, hk, key + 16 * t, held[t]);
-      const uint8_t* kp = static_cast<const uint8_t*>(g.k_codes) + row * (D * EB);
+      const uint8_t* p = static_cast<const uint8_t*>(g.k_codes) + row[t] * (D * EB) + (c * (D * EB) + q * (D / 4 * EB));
 #pragma unroll
-      for (int i = 0; i < KW; ++i) k[t][i] = ldg16(kp + c * (D * EB) + q * (D / 4 * EB) + 16 * i);
-      const uint8_t* vp = static_cast<const uint8_t*>(g.v_codes) + row * (D * EB);
+      for (int i = 0; i < KW; ++i) k[t][i] = ldg16(p + 16 * i);
+      if constexpr (SCHEME == kKvRow) ks[t] = *reinterpret_cast<const float4*>(g.k_scales + row[t] + 4 * q);
+    }
+  }
+  __device__ __forceinline__ void load_v(const AttendArgs& g, int lane) {
+    const int c = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* p = static_cast<const uint8_t*>(g.v_codes) + row[t] * (D * EB) + (4 * q * (D * EB) + c * (VW * 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         struct W { uint32_t w[VW]; };
-        const W x = *reinterpret_cast<const W*>(vp + (4 * q + i) * (D * EB) + c * (VW * 4));
+        const W x = *reinterpret_cast<const W*>(p + i * (D * EB));
 #pragma unroll
         for (int j = 0; j < VW; ++j) v[4 * t + i][j] = x.w[j];
       }
-      if constexpr (SCHEME == kKvRow) {
-        ks[t] = *reinterpret_cast<const float4*>(g.k_scales + row + 4 * q);
-        vs[t] = *reinterpret_cast<const float4*>(g.v_scales + row + 4 * q);
-      }
+    }
+  }
+  __device__ __forceinline__ void load_vs(const AttendArgs& g, int lane) {
+    if constexpr (SCHEME == kKvRow) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) vs[t] = *reinterpret_cast<const float4*>(g.v_scales + row[t] + 4 * (lane >> 4));
     }
   }
 };
 
 template <int SCHEME, int D, int NQ>
-__global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(AttendArgs g) {
-  constexpr int BM = 16 * NQ, JD = D / 16, EB = StreamTile<SCHEME, D>::EB, VW = StreamTile<SCHEME, D>::VW;
+constexpr int stream_waves() {   // per SIMD, by the registers that a wave's rows and one step's keys and values take
+  constexpr int regs = D / 4 * NQ + D / 8 * NQ + D / 4 * (SCHEME == kKvBf16 ? 2 : 1) + 72;
+  return regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+}
+
+template <int SCHEME, int D, int NQ>
+__global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend_stream(AttendArgs g) {
+  constexpr int BM = 16 * NQ, JD = D / 16, VW = StreamTile<SCHEME, D>::VW;
   __shared__ float so[4][16][D + 4];
   __shared__ float sm[4][16], sl[4][16], se[4][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -398,21 +434,30 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
   if (w.split >= mine) return;
   const int kt_first = v.kt0 + w.split * w.chunk;   // split 0 where chunk is unbounded
   const int kt_last = mine > 1 ? std::min(v.kt1, kt_first + w.chunk) : v.kt1;
-  const int G = g.H / g.Hk;
-  const int rows = w.s.n * G;
+  const int key_last = std::min(kt_last * kKeyTile, (v.end + 31) & ~31);
+  int key = kt_first * kKeyTile + 32 * wave;
+  StreamTile<SCHEME, D> x;
+  if (key < key_last) {
+    x.find(g, w.b, hk, key);
+    x.load_k(g, lane);
+    x.load_vs(g, lane);
+    x.load_v(g, lane);
+  }
 
   // this lane's rows and what they see
+  const int G = g.H / g.Hk;
+  const int rows = w.s.n * G;
   uint4 qf[NQ][D / 32];
-  int64_t row_end[NQ], row_begin[NQ];
+  int row_end[NQ], row_begin[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int r = w.tile * BM + 16 * n + c;
     const bool live = r < rows;
-    const int i = live ? r / G : 0, h = live ? hk * G + r % G : 0;
+    const int i = live ? r / G : 0, h = live ? hk * G + (r - i * G) : 0;
     const uint16_t* p = g.q + (int64_t)(w.s.first + i) * g.ldqt + (int64_t)h * g.ldqh + q4 * (D / 4);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) qf[n][j] = ldg16(p + 8 * j);
-    const int64_t pos = (int64_t)w.s.len - w.s.n + i;
+    const int pos = w.s.len - w.s.n + i;
     row_end[n] = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
     row_begin[n] = g.window ? pos - g.window + 1 : 0;
   }
@@ -428,13 +473,11 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
     for (int j = 0; j < JD; ++j) o[n][j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int64_t key_last = std::min<int64_t>((int64_t)kt_last * kKeyTile, (v.end + 31) & ~int64_t(31));
-  int64_t key = (int64_t)kt_first * kKeyTile + 32 * wave;
-  StreamTile<SCHEME, D> cur, nxt;
-  if (key < key_last) cur.load(g, w.b, hk, key, lane);
   for (; key < key_last; key += 128) {
     const bool more = key + 128 < key_last;
-    if (more) nxt.load(g, w.b, hk, key + 128, lane);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) x.held[t] = x.next_held[t];
+    if (more) x.find(g, w.b, hk, key + 128);
     // scores of 32 keys: lane (c, q4) has row c's keys 16 t + 4 q4 + i
     float s[NQ][8];
 #pragma unroll
@@ -445,9 +488,9 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         uint4 kf;
-        if constexpr (SCHEME == kKvBf16) kf = cur.k[t][j];
-        else kf = bf16x8_of((j & 1) ? make_uint2(cur.k[t][j >> 1].z, cur.k[t][j >> 1].w)
-                                    : make_uint2(cur.k[t][j >> 1].x, cur.k[t][j >> 1].y));
+        if constexpr (SCHEME == kKvBf16) kf = x.k[t][j];
+        else kf = bf16x8_of((j & 1) ? make_uint2(x.k[t][j >> 1].z, x.k[t][j >> 1].w)
+                                    : make_uint2(x.k[t][j >> 1].x, x.k[t][j >> 1].y));
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
           acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, kf), __builtin_bit_cast(v8bf, qf[n][j]),
@@ -462,8 +505,8 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
     if constexpr (SCHEME == kKvRow) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const float k4[4] = {cur.ks[t].x, cur.ks[t].y, cur.ks[t].z, cur.ks[t].w};
-        const float v4[4] = {cur.vs[t].x, cur.vs[t].y, cur.vs[t].z, cur.vs[t].w};
+        const float k4[4] = {x.ks[t].x, x.ks[t].y, x.ks[t].z, x.ks[t].w};
+        const float v4[4] = {x.vs[t].x, x.vs[t].y, x.vs[t].z, x.vs[t].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float lv;
@@ -478,17 +521,23 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[n][i] *= ks0;
     }
+    // the next step's keys come into the registers of this one's, which are done with
+    if (more) {
+      x.load_k(g, lane);
+      x.load_vs(g, lane);
+    }
     // Keys that some rows do not see: their scores go, and values that are not finite are taken out of the
     // product (0 times them is not 0) and make the scores of rows that do see them NaN.
-    const bool edge = key < v.all_begin || key + 32 > v.all_end || !cur.held[0] || !cur.held[1];
+    const bool edge = key < v.all_begin || key + 32 > v.all_end || !x.held[0] || !x.held[1];
     if (edge) {
+      asm volatile("");   // a branch: without it much of this is done for every step
       uint32_t bad = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        bool x = false;
+        bool b = false;
 #pragma unroll
-        for (int j = 0; j < VW; ++j) x |= bad_word<SCHEME>(cur.v[i][j]);
-        bad |= (uint32_t)x << i;
+        for (int j = 0; j < VW; ++j) b |= bad_word<SCHEME>(x.v[i][j]);
+        bad |= (uint32_t)b << i;
       }
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) bad |= __shfl_xor(bad, d);
@@ -496,11 +545,11 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
       for (int i = 0; i < 8; ++i) {
         const bool is_bad = (bad >> i) & 1;
 #pragma unroll
-        for (int j = 0; j < VW; ++j) cur.v[i][j] = is_bad ? 0u : cur.v[i][j];
-        const int64_t at = key + 16 * (i >> 2) + 4 * q4 + (i & 3);
+        for (int j = 0; j < VW; ++j) x.v[i][j] = is_bad ? 0u : x.v[i][j];
+        const int at = key + 16 * (i >> 2) + 4 * q4 + (i & 3);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          const bool seen = cur.held[i >> 2] && at < row_end[n] && at >= row_begin[n];
+          const bool seen = x.held[i >> 2] && at < row_end[n] && at >= row_begin[n];
           s[n][i] = !seen ? -INFINITY : is_bad ? NAN : s[n][i];
         }
         if constexpr (SCHEME == kKvRow) rv[i] = rv[i] == rv[i] ? rv[i] : 1.0f;   // such a scale's score is NaN where seen
@@ -523,17 +572,17 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
         for (int j = 0; j < JD; ++j) o[n][j] *= a;
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n] - weight_shift<SCHEME>();
-      float x[8];
+      float e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(s[n][i] - base);
+      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(s[n][i] - base);
       if (SCHEME == kKvBf16 && g.lse)
-        le[n] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-      wf[n] = make_uint4(pack_weights<SCHEME>(x[0], x[1]), pack_weights<SCHEME>(x[2], x[3]),
-                         pack_weights<SCHEME>(x[4], x[5]), pack_weights<SCHEME>(x[6], x[7]));
+        le[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      wf[n] = make_uint4(pack_weights<SCHEME>(e[0], e[1]), pack_weights<SCHEME>(e[2], e[3]),
+                         pack_weights<SCHEME>(e[4], e[5]), pack_weights<SCHEME>(e[6], e[7]));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (SCHEME == kKvRow) l[n] = __builtin_fmaf(x[i], rv[i], l[n]);
-        else l[n] += x[i];
+        if constexpr (SCHEME == kKvRow) l[n] = __builtin_fmaf(e[i], rv[i], l[n]);
+        else l[n] += e[i];
       }
     }
     // values: eight keys of D / 16 values each, transposed four by four
@@ -544,14 +593,14 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int j = 2 * u + e;
-          vf[2 * e] = make_uint4(low16s(cur.v[0][j], cur.v[1][j]), low16s(cur.v[2][j], cur.v[3][j]),
-                                 low16s(cur.v[4][j], cur.v[5][j]), low16s(cur.v[6][j], cur.v[7][j]));
-          vf[2 * e + 1] = make_uint4(high16s(cur.v[0][j], cur.v[1][j]), high16s(cur.v[2][j], cur.v[3][j]),
-                                     high16s(cur.v[4][j], cur.v[5][j]), high16s(cur.v[6][j], cur.v[7][j]));
+          vf[2 * e] = make_uint4(low16s(x.v[0][j], x.v[1][j]), low16s(x.v[2][j], x.v[3][j]),
+                                 low16s(x.v[4][j], x.v[5][j]), low16s(x.v[6][j], x.v[7][j]));
+          vf[2 * e + 1] = make_uint4(high16s(x.v[0][j], x.v[1][j]), high16s(x.v[2][j], x.v[3][j]),
+                                     high16s(x.v[4][j], x.v[5][j]), high16s(x.v[6][j], x.v[7][j]));
         }
       } else {
-        const uint32_t a[4] = {cur.v[0][u], cur.v[1][u], cur.v[2][u], cur.v[3][u]};
-        const uint32_t b[4] = {cur.v[4][u], cur.v[5][u], cur.v[6][u], cur.v[7][u]};
+        const uint32_t a[4] = {x.v[0][u], x.v[1][u], x.v[2][u], x.v[3][u]};
+        const uint32_t b[4] = {x.v[4][u], x.v[5][u], x.v[6][u], x.v[7][u]};
         uint32_t ta[4], tb[4];
         transpose4(a, ta);
         transpose4(b, tb);
@@ -564,7 +613,7 @@ __global__ __launch_bounds__(256, D * NQ <= 128 ? 2 : 1) void k_attend_stream(At
 #pragma unroll
         for (int n = 0; n < NQ; ++n) o[n][4 * u + e] = mfma16_pv<SCHEME>(vf[e], wf[n], o[n][4 * u + e]);
     }
-    if (more) cur = nxt;
+    if (more) x.load_v(g, lane);
   }
 
   // join the four waves, 16 rows at a time: lane (c, q4) holds row c's values (4 q4 + i) D / 16 + j
@@ -642,7 +691,7 @@ struct KeyTile {
     return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1);
   }
 
-  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int64_t key) {
+  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int key) {
     const int t = threadIdx.x;
     int64_t base[KT / 16];
     held = 0;
@@ -785,21 +834,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   const int row = w.tile * BM + 32 * wave + c;
   const bool live = row < rows;
   const bool wave_live = w.tile * BM + 32 * wave < rows;
-  const int i = live ? row / G : 0, h = live ? hk * G + row % G : 0;
+  const int i = live ? row / G : 0, h = live ? hk * G + (row - i * G) : 0;
   uint4 qf[D / 16];
   {
     const uint16_t* p = g.q + (int64_t)(w.s.first + i) * g.ldqt + (int64_t)h * g.ldqh + 8 * h2;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) qf[j] = ldg16(p + 16 * j);
   }
-  const int64_t pos = (int64_t)w.s.len - w.s.n + i;
-  const int64_t row_end = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
-  const int64_t row_begin = g.window ? pos - g.window + 1 : 0;
+  const int pos = w.s.len - w.s.n + i;
+  const int row_end = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
+  const int row_begin = g.window ? pos - g.window + 1 : 0;
   // the last key that any row of this wave sees, and the first
   const int last = std::min(rows, w.tile * BM + 32 * wave + 32) - 1;
-  const int64_t wave_end = g.causal ? std::min(v.end, (int64_t)w.s.len - w.s.n + last / G + 1) : v.end;
-  const int64_t wave_begin =
-      g.window ? (int64_t)w.s.len - w.s.n + (w.tile * BM + 32 * wave) / G - g.window + 1 : 0;
+  const int wave_end = g.causal ? std::min(v.end, w.s.len - w.s.n + last / G + 1) : v.end;
+  const int wave_begin = g.window ? w.s.len - w.s.n + (w.tile * BM + 32 * wave) / G - g.window + 1 : 0;
 
   const float ks0 = score_scale<SCHEME>(g);
   v16f o[ND];
@@ -809,10 +857,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
     for (int r = 0; r < 16; ++r) o[j][r] = 0.0f;
   float m = -INFINITY, l = 0.0f, le = 0.0f;   // le: bf16 caches, weights before their rounding
 
-  const int64_t key_first = (int64_t)kt_first * kKeyTile;
-  const int64_t key_last = std::min<int64_t>((int64_t)kt_last * kKeyTile, (v.end + KT - 1) / KT * KT);
-  const int tiles = key_last > key_first ? (int)((key_last - key_first) / KT) : 0;
-  auto is_edge = [&](int64_t key, uint32_t held) {
+  const int key_first = kt_first * kKeyTile;
+  const int key_last = std::min(kt_last * kKeyTile, (v.end + KT - 1) / KT * KT);
+  const int tiles = key_last > key_first ? (key_last - key_first) / KT : 0;
+  auto is_edge = [&](int key, uint32_t held) {
     return key < v.all_begin || key + KT > v.all_end || held != (1u << (KT / 16)) - 1;
   };
   if (threadIdx.x < KT) marks[0][threadIdx.x] = marks[1][threadIdx.x] = -1;
@@ -830,7 +878,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   for (int x = 0; x < tiles; ++x) {
     __syncthreads();
     const int buf = x & 1;
-    const int64_t key = key_first + (int64_t)x * KT;
+    const int key = key_first + x * KT;
     const bool edge = is_edge(key, held);
     const uint32_t held_now = held;
     if (x + 1 < tiles) {
@@ -873,6 +921,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
       }
     }
     if (edge) {
+      asm volatile("");   // a branch
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -982,43 +1031,77 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
 }
 
 // ---------------------------------------------------------------- join
-// The rows of a tile whose keys were cut into several ranges: the ranges' sums, each at its own maximum.
-template <int SCHEME, int BM>
+// The rows of a tile whose keys were cut into several ranges: the ranges' sums, each at its own maximum.  RW
+// rows per workgroup; the threads of a row, D / 8 across, share its ranges out among them and meet in LDS.
+template <int SCHEME, int BM, int D>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
+  constexpr int RW = BM == 128 ? 4 : 1, TR = D / 8, NG = 256 / TR / RW;   // groups of threads per row
+  constexpr int U = 4;                                                    // ranges in flight
+  __shared__ float so[RW][NG][D + 4];
+  __shared__ float sm[RW][NG], sl[RW][NG], se[RW][NG];
   const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
   Work w;
   if (!find_work<BM, true>(g, blockIdx.x / (uint32_t)g.Hk, w)) return;
+  const int rows = w.s.n * (g.H / g.Hk), r_first = (int)blockIdx.y * RW;
+  if (w.tile * BM + r_first >= rows) return;
   const Sight v = sight_of<BM>(g, w.s, w.tile);
   const int mine = splits_of(v.kt1 - v.kt0, w.chunk);
   if (mine < 2 || (uint64_t)w.part + (uint64_t)mine > (uint64_t)g.parts) return;
-  const int G = g.H / g.Hk, rows = w.s.n * G, tr = g.D / 8, rp = 256 / tr;
-  const int d = (int)(threadIdx.x % (uint32_t)tr) * 8, r0 = (int)(threadIdx.x / (uint32_t)tr);
-  if (r0 >= rp) return;
-  const float fin = final_scale<SCHEME>(g);
-  for (int r = r0; r < BM; r += rp) {
-    const int row = w.tile * BM + r;
-    if (row >= rows) return;
+  const int tr = (int)(threadIdx.x % TR), group = (int)(threadIdx.x / TR) % NG, ri = (int)(threadIdx.x / (TR * NG));
+  const int r = r_first + ri, row = w.tile * BM + r;
+  const bool live = ri < RW && row < rows;
+  if (live) {
+    const float4* ml = part_ml(g, BM, D, hk, w.part, r);
+    const float* sums = part_sums(g, BM, D, hk, w.part, r) + 8 * tr;
     float top = -INFINITY;
-    for (int x = 0; x < mine; ++x) top = fmaxf(top, part_ml(g, BM, g.D, hk, w.part + x, r)->x);
+    for (int x = group; x < mine; x += NG) top = fmaxf(top, ml[(int64_t)x * BM].x);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
-    for (int x = 0; x < mine; ++x) {
-      const float4 ml = *part_ml(g, BM, g.D, hk, w.part + x, r);
-      const float f = join_factor(ml.x, ml.y, top);
-      const float* p = part_sums(g, BM, g.D, hk, w.part + x, r) + d;
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      sum = __builtin_fmaf(f, ml.y, sum);
-      exact = __builtin_fmaf(f, ml.z, exact);
-      acc[0] = __builtin_fmaf(f, a.x, acc[0]);
-      acc[1] = __builtin_fmaf(f, a.y, acc[1]);
-      acc[2] = __builtin_fmaf(f, a.z, acc[2]);
-      acc[3] = __builtin_fmaf(f, a.w, acc[3]);
-      acc[4] = __builtin_fmaf(f, b.x, acc[4]);
-      acc[5] = __builtin_fmaf(f, b.y, acc[5]);
-      acc[6] = __builtin_fmaf(f, b.z, acc[6]);
-      acc[7] = __builtin_fmaf(f, b.w, acc[7]);
+    for (int x0 = group; x0 < mine; x0 += NG * U) {
+      float4 p[U], a[U], b[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = (int64_t)std::min(x0 + u * NG, mine - 1) * BM;
+        p[u] = ml[at];
+        a[u] = *reinterpret_cast<const float4*>(sums + at * D);
+        b[u] = *reinterpret_cast<const float4*>(sums + at * D + 4);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (x0 + u * NG >= mine) break;
+        const float f = join_factor(p[u].x, p[u].y, top);
+        sum = __builtin_fmaf(f, p[u].y, sum);
+        exact = __builtin_fmaf(f, p[u].z, exact);
+        acc[0] = __builtin_fmaf(f, a[u].x, acc[0]);
+        acc[1] = __builtin_fmaf(f, a[u].y, acc[1]);
+        acc[2] = __builtin_fmaf(f, a[u].z, acc[2]);
+        acc[3] = __builtin_fmaf(f, a[u].w, acc[3]);
+        acc[4] = __builtin_fmaf(f, b[u].x, acc[4]);
+        acc[5] = __builtin_fmaf(f, b[u].y, acc[5]);
+        acc[6] = __builtin_fmaf(f, b[u].z, acc[6]);
+        acc[7] = __builtin_fmaf(f, b[u].w, acc[7]);
+      }
     }
-    store_row<SCHEME>(g, w.s, row, hk, d, acc, top, sum, exact, fin);
+    if (tr == 0) {
+      sm[ri][group] = top;
+      sl[ri][group] = sum;
+      se[ri][group] = exact;
+    }
+    *reinterpret_cast<float4*>(&so[ri][group][8 * tr]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *reinterpret_cast<float4*>(&so[ri][group][8 * tr + 4]) = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
+  __syncthreads();
+  if (!live || group != 0) return;
+  float top = -INFINITY;
+  for (int x = 0; x < NG; ++x) top = fmaxf(top, sm[ri][x]);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
+  for (int x = 0; x < NG; ++x) {
+    const float f = join_factor(sm[ri][x], sl[ri][x], top);
+    sum = __builtin_fmaf(f, sl[ri][x], sum);
+    exact = __builtin_fmaf(f, se[ri][x], exact);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[ri][x][8 * tr + e], acc[e]);
+  }
+  store_row<SCHEME>(g, w.s, row, hk, 8 * tr, acc, top, sum, exact, final_scale<SCHEME>(g));
 }
 
 // ---------------------------------------------------------------- choice and launch
@@ -1055,10 +1138,10 @@ hipError_t attend_with(AttendArgs& g, const Plan& p, hipStream_t st) {
   else hipLaunchKernelGGL((k_attend_tile<SCHEME, D>), grid, dim3(256), 0, st, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.target == 0) return e;
-  const dim3 joins((unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk));
-  if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16>), joins, dim3(256), 0, st, g);
-  else if (p.bm == 32) hipLaunchKernelGGL((k_attend_join<SCHEME, 32>), joins, dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((k_attend_join<SCHEME, 128>), joins, dim3(256), 0, st, g);
+  const unsigned joins = (unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk);
+  if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D>), dim3(joins, 16), dim3(256), 0, st, g);
+  else if (p.bm == 32) hipLaunchKernelGGL((k_attend_join<SCHEME, 32, D>), dim3(joins, 32), dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D>), dim3(joins, 32), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 

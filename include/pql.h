@@ -423,7 +423,7 @@ const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, in
  *
  * A cache holds n_pages pages of page_size tokens (a power of two, 16 .. 2^16;
  * n_pages * page_size <= 2^31 - 1) for Hk heads of D values, D one of 64, 128,
- * 192, 256:
+ * 192, 256, a page of all heads below 2^31 bytes:
  *   KV_BF16        k, v bf16 [n_pages, Hk, page_size, D]            no scales
  *   KV_FP8_TENSOR  k, v e4m3fn codes of the same shape              scales f32 [1] each,
  *                                                                   given by the caller

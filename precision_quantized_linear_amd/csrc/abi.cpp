@@ -1119,6 +1119,9 @@ pql_status check_cache(int scheme, int64_t n_pages, int64_t page_size, int64_t H
     return fail(PQL_ERR_INVALID_ARGUMENT, "page_size must be a power of two, 16 .. 65536 (got %lld)", (long long)page_size);
   if (n_pages < 1 || n_pages > kInt31 / page_size)
     return fail(PQL_ERR_INVALID_ARGUMENT, "n_pages must be 1 .. (2^31 - 1) / page_size (got %lld)", (long long)n_pages);
+  if (Hk >= 1 && Hk > ((int64_t(1) << 31) - 1) / (page_size * D * (scheme == PQL_KV_BF16 ? 2 : 1)))
+    return fail(PQL_ERR_INVALID_ARGUMENT, "a page of %lld heads of %lld x %lld values must stay below 2^31 bytes",
+                (long long)Hk, (long long)page_size, (long long)D);
   if (Hk < 1 || Hk > kMaxSpan / (n_pages * page_size * D))
     return fail(PQL_ERR_INVALID_ARGUMENT, "a cache of %lld x %lld x %lld x %lld is too large or has no heads",
                 (long long)n_pages, (long long)Hk, (long long)page_size, (long long)D);

@@ -663,25 +663,24 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
 }
 
 // ---------------------------------------------------------------- many rows: key tiles through LDS
-// 128 rows per workgroup, 32 to a wave, 32 x 32 x 16 matrix instructions.  A tile of 64 keys (32 where a head has
-// more than 128 values) is read into registers one tile ahead, turned into 16-bit operands once for all four
-// waves on its way to LDS (values transposed, so that a fragment of both operands is one 16-byte read), and
-// double-buffered: one barrier per tile.  Two workgroups share a CU, one's softmax beside the
-// other's products.
+// Four waves of 32 rows, 32 x 32 x 16 matrix instructions.  A tile of 64 keys (32 where a head has more than 128
+// values) is read into registers one tile ahead, turned into 16-bit operands once for all four waves on its
+// way to LDS (values transposed, so that a fragment of either operand is one 16-byte read), and
+// double-buffered: one barrier per tile.
 template <int SCHEME, int D>
 struct KeyTile {
+  static constexpr int NT = 256;                              // threads
   static constexpr int KT = D <= 128 ? 64 : 32;
   static constexpr int EB = SCHEME == kKvBf16 ? 2 : 1;
   static constexpr int PK = D * EB / 16;                      // 16-byte pieces of a key
-  static constexpr int NK = (KT * PK + 255) / 256;            // pieces per thread
+  static constexpr int NK = (KT * PK + NT - 1) / NT;            // pieces per thread
   static constexpr int UV = KT / 4 * (D / 4);                 // units of 4 keys x 4 values
-  static constexpr int NV = (UV + 255) / 256;
+  static constexpr int NV = (UV + NT - 1) / NT;
   static constexpr int kBytes = KT * D * 2;                   // of one operand in LDS
 
   uint4 k[NK];
   uint2 v[NV][4];                                             // FP8: .x alone
   float ks, vs;
-  uint32_t held;                                              // a bit per 16 keys
 
   static __device__ __forceinline__ int v_dq(int e) { return e % (D / 4); }
   // Units 2 apart in a group of four keys' order lie in the two halves of a 16-byte chunk: lanes of a wave
@@ -691,43 +690,60 @@ struct KeyTile {
     return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1);
   }
 
-  __device__ __forceinline__ void load(const AttendArgs& g, int b, int hk, int key) {
+  // Lane i's page of the tile's keys 16 i .. 16 i + 15 (page 0, and a bit off in `held`, where the cache has none).
+  int page;
+  uint32_t held;
+  __device__ __forceinline__ void find(const AttendArgs& g, int b, int key) {
+    const int i = threadIdx.x & (KT / 16 - 1);
+    const int p = (key + 16 * i) >> g.page_shift, last_page = (int)g.width - 1;
+    const int at = g.pages[b * g.ldp + std::min(p, last_page)];
+    const bool there = at >= 0 && at < g.n_pages && p <= last_page;
+    page = there ? at : 0;
+    held = (uint32_t)__ballot(there) & ((1u << (KT / 16)) - 1);
+  }
+  // Bytes from the head's first value in page 0 to the tile's key 16 i, i the group of 16 keys that r lies in.  A
+  // wave's piece or unit falls into one such group for all of its lanes, at every head size, so this is a
+  // scalar.  A page of all heads is below 2^31 bytes.
+  __device__ __forceinline__ uint64_t at(const AttendArgs& g, int key, int r) const {
+    const int i = __builtin_amdgcn_readfirstlane(r >> 4);
+    const uint32_t p = (uint32_t)__builtin_amdgcn_readlane(page, i);
+    const uint32_t page_bytes = ((uint32_t)g.Hk << g.page_shift) * (uint32_t)(D * EB);
+    return (uint64_t)p * page_bytes + (uint32_t)((key + 16 * i) & ((1 << g.page_shift) - 1)) * (uint32_t)(D * EB);
+  }
+  // Codes of one byte at 64 or 128 values: a thread's pieces of keys and units of values are of the same 16 keys.
+  static constexpr bool kSameGroup = EB == 1 && D <= 128;
+
+  __device__ __forceinline__ void load(const AttendArgs& g, int hk, int key) {
     const int t = threadIdx.x;
-    int64_t base[KT / 16];
-    held = 0;
-#pragma unroll
-    for (int i = 0; i < KT / 16; ++i) {
-      bool h;
-      base[i] = rows_at(g, b, hk, key + 16 * i, h);
-      held |= (uint32_t)h << i;
-    }
-    auto row_of = [&](int r) {   // cache row of the tile's key r
-      int64_t x = base[0];
-#pragma unroll
-      for (int i = 1; i < KT / 16; ++i) x = (r >> 4) == i ? base[i] : x;
-      return x + (r & 15);
-    };
+    const uint64_t head = ((uint64_t)hk << g.page_shift) * (D * EB);
+    const uint8_t* kp = static_cast<const uint8_t*>(g.k_codes) + head;
+    const uint8_t* vp = static_cast<const uint8_t*>(g.v_codes) + head;
+    uint64_t from[NK];
 #pragma unroll
     for (int u = 0; u < NK; ++u) {
-      const int e = t + 256 * u;
-      if (KT * PK % 256 == 0 || e < KT * PK)
-        k[u] = ldg16(static_cast<const uint8_t*>(g.k_codes) + row_of(e / PK) * (D * EB) + (e % PK) * 16);
+      const int e = t + NT * u;
+      if (KT * PK % NT == 0 || e < KT * PK) {
+        from[u] = at(g, key, e / PK);
+        k[u] = ldg16(kp + from[u] + (uint32_t)((e / PK & 15) * (D * EB) + (e % PK) * 16));
+      }
     }
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int e = t + 256 * u;
-      if (UV % 256 == 0 || e < UV) {
-        const uint8_t* p = static_cast<const uint8_t*>(g.v_codes) + row_of(4 * v_kg(e)) * (D * EB) + v_dq(e) * (4 * EB);
+      const int e = t + NT * u;
+      if (UV % NT == 0 || e < UV) {
+        const int r = 4 * v_kg(e);
+        const uint8_t* q = vp + (kSameGroup ? from[u] : at(g, key, r)) + (uint32_t)((r & 15) * (D * EB) + v_dq(e) * (4 * EB));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (SCHEME == kKvBf16) v[u][i] = *reinterpret_cast<const uint2*>(p + i * (D * EB));
-          else v[u][i].x = *reinterpret_cast<const uint32_t*>(p + i * (D * EB));
+          if constexpr (SCHEME == kKvBf16) v[u][i] = *reinterpret_cast<const uint2*>(q + i * (D * EB));
+          else v[u][i].x = *reinterpret_cast<const uint32_t*>(q + i * (D * EB));
         }
       }
     }
     if constexpr (SCHEME == kKvRow) {
       if (t < KT) {
-        const int64_t r = row_of(t);
+        const int64_t r = (((int64_t)__shfl(page, t >> 4) * g.Hk + hk) << g.page_shift) +
+                          ((key + t) & ((1 << g.page_shift) - 1));
         ks = g.k_scales[r];
         vs = g.v_scales[r];
       }
@@ -747,40 +763,55 @@ struct KeyTile {
     return v_row(d) + (((2 * (kg >> 2) + (kg & 1)) ^ v_swizzle(d)) << 4) + ((kg >> 1) & 1) * 8;
   }
 
-  // edge: some row does not see every key of the tile.  Values that are not finite are then left out, and their
-  // key is marked with the tile's number.
-  __device__ __forceinline__ void store(uint8_t* kl, uint8_t* vl, float* params, int* marks, bool edge, int number,
-                                        float ks0) {
+  // A thread's places in LDS: k0 of its first piece, v0 of its first unit.  Up to 128 values the others follow
+  // from these: the next piece is whole periods of the swizzle of rows further, the second half of a piece, the
+  // next two values of a unit and the next unit differ in one bit of the chunk.
+  static constexpr bool kNear = D <= 128;
+  static __device__ __forceinline__ int k_first() { return k_at(threadIdx.x / PK, (threadIdx.x % PK) * (2 / EB)); }
+  static __device__ __forceinline__ int v_first() { return v_at(4 * v_dq(threadIdx.x), v_kg(threadIdx.x)); }
+  __device__ __forceinline__ void store_k(uint8_t* kl, int k0) const {
     const int t = threadIdx.x;
 #pragma unroll
     for (int u = 0; u < NK; ++u) {
-      const int e = t + 256 * u;
-      if (KT * PK % 256 == 0 || e < KT * PK) {
-        const int r = e / PK, c = e % PK;
+      const int e = t + NT * u;
+      if (KT * PK % NT == 0 || e < KT * PK) {
+        const int r = e / PK, c = (e % PK) * (2 / EB);
+        const int at = kNear ? k0 + u * (NT / PK) * (D * 2) : k_at(r, c);
         if constexpr (SCHEME == kKvBf16) {
-          stg16(kl + k_at(r, c), k[u]);
+          stg16(kl + at, k[u]);
         } else {
-          stg16(kl + k_at(r, 2 * c), bf16x8_of(make_uint2(k[u].x, k[u].y)));
-          stg16(kl + k_at(r, 2 * c + 1), bf16x8_of(make_uint2(k[u].z, k[u].w)));
+          stg16(kl + at, bf16x8_of(make_uint2(k[u].x, k[u].y)));
+          stg16(kl + (kNear ? (k0 ^ 16) + u * (NT / PK) * (D * 2) : k_at(r, c + 1)), bf16x8_of(make_uint2(k[u].z, k[u].w)));
         }
       }
     }
+  }
+  // Values that are not finite are taken out, and their key is marked with the tile's number (a tile of which
+  // some row does not see every key: 0 times such a value is not 0).
+  __device__ __forceinline__ void clean_v(int* marks, int number) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int e = t + 256 * u;
-      if (UV % 256 == 0 || e < UV) {
-        const int d0 = 4 * v_dq(e), kg = v_kg(e);
-        if (edge) {
+      const int e = threadIdx.x + NT * u;
+      if (UV % NT == 0 || e < UV) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bool bad = bad_word<SCHEME>(v[u][i].x);
-            if constexpr (SCHEME == kKvBf16) bad |= bad_word<SCHEME>(v[u][i].y);
-            if (bad) {
-              v[u][i] = make_uint2(0u, 0u);
-              marks[4 * kg + i] = number;
-            }
+        for (int i = 0; i < 4; ++i) {
+          bool bad = bad_word<SCHEME>(v[u][i].x);
+          if constexpr (SCHEME == kKvBf16) bad |= bad_word<SCHEME>(v[u][i].y);
+          if (bad) {
+            v[u][i] = make_uint2(0u, 0u);
+            marks[4 * v_kg(e) + i] = number;
           }
         }
+      }
+    }
+  }
+  __device__ __forceinline__ void store_v(uint8_t* vl, int v0, float* params, float ks0) const {
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int e = t + NT * u;
+      if (UV % NT == 0 || e < UV) {
+        const int d0 = 4 * v_dq(e), kg = v_kg(e);
         uint2 out[4];
         if constexpr (SCHEME == kKvBf16) {
           out[0] = make_uint2(low16s(v[u][0].x, v[u][1].x), low16s(v[u][2].x, v[u][3].x));
@@ -795,7 +826,8 @@ struct KeyTile {
           for (int i = 0; i < 4; ++i) out[i] = make_uint2(f16x2_of(ta[i], false), f16x2_of(ta[i], true));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) stg8(vl + v_at(d0 + i, kg), out[i]);
+        for (int i = 0; i < 4; ++i)   // at 128 values the next unit is 8 groups of keys on: 4 chunks
+          stg8(vl + (kNear ? (v0 ^ ((i >> 1) << 4 | u << 6)) + i * (KT * 2) : v_at(d0 + i, kg)), out[i]);
       }
     }
     if constexpr (SCHEME == kKvRow) {
@@ -866,12 +898,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   if (threadIdx.x < KT) marks[0][threadIdx.x] = marks[1][threadIdx.x] = -1;
   __syncthreads();
   Tile next;
-  uint32_t held = 0;
+  uint32_t held = 0, held_next = 0;
+  const int k0 = Tile::k_first(), v0 = Tile::v_first();
+  auto put = [&](int x, int key) {   // the registers' tile x to LDS
+    if (is_edge(key, held_next)) next.clean_v(marks[x & 1], x);
+    next.store_k(lds_k[x & 1], k0);
+    next.store_v(lds_v[x & 1], v0, params[x & 1], ks0);
+  };
+  auto get = [&](int key) {          // the tile at `key` to the registers, and the pages of the one behind it
+    next.load(g, hk, key);
+    held_next = next.held;
+    next.find(g, w.b, std::min(key + KT, key_last - KT));
+  };
   if (tiles > 0) {
-    next.load(g, w.b, hk, key_first);
-    held = next.held;
-    next.store(lds_k[0], lds_v[0], params[0], marks[0], is_edge(key_first, held), 0, ks0);
-    if (tiles > 1) next.load(g, w.b, hk, key_first + KT);
+    next.find(g, w.b, key_first);
+    get(key_first);
+    held = held_next;
+    put(0, key_first);
+    if (tiles > 1) get(key_first + KT);
   }
   const int k_lane = Tile::k_at(c, h2);            // key c's chunk h2; chunk 2 j + h2 is an exclusive or away
   constexpr int kGroup = D % 128 == 0 ? 8 : 4;     // fragments whose chunks the swizzle permutes among themselves
@@ -882,25 +926,26 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
     const bool edge = is_edge(key, held);
     const uint32_t held_now = held;
     if (x + 1 < tiles) {
-      held = next.held;
-      next.store(lds_k[buf ^ 1], lds_v[buf ^ 1], params[buf ^ 1], marks[buf ^ 1], is_edge(key + KT, held), x + 1, ks0);
-      if (x + 2 < tiles) next.load(g, w.b, hk, key + 2 * KT);
+      held = held_next;
+      put(x + 1, key + KT);
+      if (x + 2 < tiles) get(key + 2 * KT);
     }
     if (!wave_live || key >= wave_end || key + KT <= wave_begin) continue;
     const uint8_t* kl = lds_k[buf];
     const uint8_t* vl = lds_v[buf];
     v16f s[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
         const uint4 kf = ldg16(kl + b * 32 * (D * 2) + j / kGroup * (32 * kGroup) + (k_lane ^ (j % kGroup << 5)));
         s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, kf), __builtin_bit_cast(v8bf, qf[j]), s[b],
                                                        0, 0, 0);
       }
-    }
     // lane (c, h2) has row c's keys 32 b + 8 (r / 4) + 4 h2 + r % 4
     const float* pr = params[buf];
 #pragma unroll
@@ -1033,9 +1078,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
 // ---------------------------------------------------------------- join
 // The rows of a tile whose keys were cut into several ranges: the ranges' sums, each at its own maximum.  RW
 // rows per workgroup; the threads of a row, D / 8 across, share its ranges out among them and meet in LDS.
-template <int SCHEME, int BM, int D>
+template <int SCHEME, int BM, int D, int RW>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
-  constexpr int RW = BM == 128 ? 4 : 1, TR = D / 8, NG = 256 / TR / RW;   // groups of threads per row
+  constexpr int TR = D / 8, NG = 256 / TR / RW;   // groups of threads per row
   constexpr int U = 4;                                                    // ranges in flight
   __shared__ float so[RW][NG][D + 4];
   __shared__ float sm[RW][NG], sl[RW][NG], se[RW][NG];
@@ -1054,7 +1099,6 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
     const float4* ml = part_ml(g, BM, D, hk, w.part, r);
     const float* sums = part_sums(g, BM, D, hk, w.part, r) + 8 * tr;
     float top = -INFINITY;
-    for (int x = group; x < mine; x += NG) top = fmaxf(top, ml[(int64_t)x * BM].x);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
     for (int x0 = group; x0 < mine; x0 += NG * U) {
       float4 p[U], a[U], b[U];
@@ -1065,6 +1109,15 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
         a[u] = *reinterpret_cast<const float4*>(sums + at * D);
         b[u] = *reinterpret_cast<const float4*>(sums + at * D + 4);
       }
+      float next = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) next = fmaxf(next, x0 + u * NG < mine ? p[u].x : -INFINITY);
+      const float old = join_factor(top, sum, next);
+      top = next;
+      sum *= old;
+      exact *= old;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (x0 + u * NG >= mine) break;
@@ -1139,9 +1192,11 @@ hipError_t attend_with(AttendArgs& g, const Plan& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.target == 0) return e;
   const unsigned joins = (unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk);
-  if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D>), dim3(joins, 16), dim3(256), 0, st, g);
-  else if (p.bm == 32) hipLaunchKernelGGL((k_attend_join<SCHEME, 32, D>), dim3(joins, 32), dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D>), dim3(joins, 32), dim3(256), 0, st, g);
+  if (p.bm == 128) hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D, 4>), dim3(joins, 32), dim3(256), 0, st, g);
+  else if (joins < 64 && p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D, 1>), dim3(joins, 16), dim3(256), 0, st, g);
+  else if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D, 4>), dim3(joins, 4), dim3(256), 0, st, g);
+  else if (joins < 64) hipLaunchKernelGGL((k_attend_join<SCHEME, 32, D, 1>), dim3(joins, 32), dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((k_attend_join<SCHEME, 32, D, 4>), dim3(joins, 8), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 

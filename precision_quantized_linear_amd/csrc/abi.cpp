@@ -1375,6 +1375,7 @@ static pql_status attend_shape(int scheme, int64_t T, int64_t H, int64_t Hk, int
     return fail(PQL_ERR_INVALID_ARGUMENT, "H = %lld must be a multiple of Hk = %lld", (long long)H, (long long)Hk);
   if ((st = check_batch(B, width, width, page_size)) != PQL_OK) return st;
   *g = pql::AttendArgs{};
+  g->scheme = scheme;
   g->T = T;
   g->H = (int)H;
   g->Hk = (int)Hk;
@@ -1461,7 +1462,7 @@ static pql_status kv_attention_impl(int scheme, const void* q, int64_t ldqt, int
   g.ldoh = ldoh;
   g.lse = lse;
   g.ws = static_cast<float*>(workspace);
-  return launched(pql::launch_kv_attention(scheme, g, static_cast<hipStream_t>(stream)), "kv_attention launch");
+  return launched(pql::launch_kv_attention(g, static_cast<hipStream_t>(stream)), "kv_attention launch");
 }
 
 pql_status pql_kv_attention(int scheme, const void* q, int64_t ldqt, int64_t ldqh, int64_t T, int64_t H,

@@ -38,14 +38,14 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRise = 8.0f;       // m follows the maximum when that is so much higher
-constexpr float kSmallestValueScale = 0x1p-100f;
+constexpr float kSmallestValueScale = 0x1p-100f, kSmallestLog = -100.0f;
 
 template <int SCHEME>
 constexpr float weight_shift() { return SCHEME == kKvBf16 ? 0.0f : 7.0f; }
 
 // ---------------------------------------------------------------- work of a workgroup
 // Tiles of BM rows; keys in tiles of 64.  A sequence's row tiles are each cut into `splits` ranges of `chunk`
-// key tiles, the chunk chosen on the device so that all ranges of all heads are about `target`: long
+// key tiles at most, the chunk chosen on the device so that all ranges of all heads are about `target`: long
 // contexts are spread over the card whatever the others' lengths.  Every workgroup finds its own sequence by
 // a scan over the batch, 4 sequences per lane and step.
 constexpr int kKeyTile = 64;
@@ -149,7 +149,7 @@ __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Wor
     const uint64_t hit = __ballot(idx >= at && idx - at < mine);
     if (hit) {
       const int who = __builtin_ctzll(hit);
-      int found = 0, found_splits = 1, found_qt = 0;
+      int found = 0, found_splits = 1, found_qt = 0, found_kt = 0;
       Seq found_s{0, 0, 0};
       uint32_t rest = 0, found_parts = 0;
 #pragma unroll
@@ -158,6 +158,7 @@ __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Wor
           found = b0 + 4 * lane + r;
           found_splits = splits[r];
           found_qt = x.qt[r];
+          found_kt = x.kt[r];
           found_s = x.s[r];
           rest = idx - at;
           found_parts = at_parts;
@@ -172,7 +173,8 @@ __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Wor
       const int qt = __builtin_amdgcn_readlane(found_qt, who);
       rest = (uint32_t)__builtin_amdgcn_readlane((int)rest, who);
       found_parts = (uint32_t)__builtin_amdgcn_readlane((int)found_parts, who);
-      w.chunk = chunk;
+      const uint32_t kt = (uint32_t)__builtin_amdgcn_readlane(found_kt, who);
+      w.chunk = splits_b == 1 ? chunk : (int)((kt + splits_b - 1) / splits_b);   // of equal length
       // the last tile sees most: it goes first
       const uint32_t j = MULTI || splits_b == 1 ? rest : rest / splits_b;
       w.tile = qt - 1 - (int)j;
@@ -290,10 +292,14 @@ __device__ __forceinline__ bool bad_codes(uint32_t c) {
 __device__ __forceinline__ bool bad_bf16(uint32_t c) {
   return (c & 0x7F80u) == 0x7F80u || (c & 0x7F800000u) == 0x7F800000u;
 }
+__device__ __forceinline__ uint32_t magnitude(uint32_t codes) { return codes & 0x7F7F7F7Fu; }
 template <int SCHEME>
 __device__ __forceinline__ bool bad_word(uint32_t c) { return SCHEME == kKvBf16 ? bad_bf16(c) : bad_codes(c); }
 
-// A value scale as the weights take it: its logarithm and its reciprocal.
+// A value scale as the weights take it: its logarithm and its reciprocal.  Callers look for rows of zeros where a
+// scale is 1: the quantizer's rule gives them that, which says nothing about their size and would lift m above all
+// weights that matter where the others' values are small.  Such a key has no weight (its logarithm is the
+// smallest scale's, its reciprocal 0) and adds 2^(s - m) to l by itself.
 __device__ __forceinline__ void value_scale(float vs, float& lv, float& rv) {
   vs = vs < kSmallestValueScale ? kSmallestValueScale : vs;   // a NaN stays one
   lv = __builtin_amdgcn_logf(vs);
@@ -502,6 +508,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
         for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[n][i];
     }
     float rv[8];
+    uint32_t ones = 0;      // keys whose value scale is 1, then those whose values are all zero
     if constexpr (SCHEME == kKvRow) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -509,10 +516,28 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
         const float v4[4] = {x.vs[t].x, x.vs[t].y, x.vs[t].z, x.vs[t].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          ones |= (uint32_t)(v4[i] == 1.0f) << (4 * t + i);
           float lv;
           value_scale(v4[i], lv, rv[4 * t + i]);
 #pragma unroll
           for (int n = 0; n < NQ; ++n) s[n][4 * t + i] = __builtin_fmaf(s[n][4 * t + i], k4[i] * ks0, lv);
+        }
+      }
+      if (__any(ones)) {
+        asm volatile("");   // a branch
+        uint32_t some = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) some |= magnitude(x.v[i][j]) ? 1u << i : 0u;
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) some |= __shfl_xor(some, d);
+        ones &= ~some;      // rows of zeros; the logarithm of 1 is 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (ones >> i & 1) rv[i] = 0.0f;
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][i] += ones >> i & 1 ? kSmallestLog : 0.0f;
         }
       }
     } else {
@@ -572,6 +597,14 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
         for (int j = 0; j < JD; ++j) o[n][j] *= a;
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n] - weight_shift<SCHEME>();
+      if constexpr (SCHEME == kKvRow) {
+        if (__any(ones)) {
+          asm volatile("");   // a branch
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (ones >> i & 1) l[n] += __builtin_amdgcn_exp2f(s[n][i] - kSmallestLog - base);
+        }
+      }
       float e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(s[n][i] - base);
@@ -680,7 +713,8 @@ struct KeyTile {
 
   uint4 k[NK];
   uint2 v[NV][4];                                             // FP8: .x alone
-  float ks, vs;
+  float ks, vs;                                               // of key threadIdx.x, in `row` of the cache
+  int64_t row;
 
   static __device__ __forceinline__ int v_dq(int e) { return e % (D / 4); }
   // Units 2 apart in a group of four keys' order lie in the two halves of a 16-byte chunk: lanes of a wave
@@ -742,10 +776,9 @@ struct KeyTile {
     }
     if constexpr (SCHEME == kKvRow) {
       if (t < KT) {
-        const int64_t r = (((int64_t)__shfl(page, t >> 4) * g.Hk + hk) << g.page_shift) +
-                          ((key + t) & ((1 << g.page_shift) - 1));
-        ks = g.k_scales[r];
-        vs = g.v_scales[r];
+        row = (((int64_t)__shfl(page, t >> 4) * g.Hk + hk) << g.page_shift) + ((key + t) & ((1 << g.page_shift) - 1));
+        ks = g.k_scales[row];
+        vs = g.v_scales[row];
       }
     }
   }
@@ -805,7 +838,8 @@ struct KeyTile {
       }
     }
   }
-  __device__ __forceinline__ void store_v(uint8_t* vl, int v0, float* params, float ks0) const {
+  __device__ __forceinline__ void store_v(const AttendArgs& g, uint8_t* vl, int v0, float* params, float ks0, int* zeros,
+                                          int number) const {
     const int t = threadIdx.x;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
@@ -834,6 +868,16 @@ struct KeyTile {
       if (t < KT) {
         float lv, rv;
         value_scale(vs, lv, rv);
+        if (vs == 1.0f) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g.v_codes) + row * D);
+          uint32_t some = 0;
+          for (int i = 0; i < D / 16; ++i) some |= magnitude(p[i].x | p[i].y | p[i].z | p[i].w);
+          if (!some) {
+            lv = kSmallestLog;
+            rv = 0.0f;
+            *zeros = number;
+          }
+        }
         params[t] = ks * ks0;
         params[KT + t] = lv;
         params[2 * KT + t] = rv == rv ? rv : 1.0f;   // such a scale's score is NaN where seen
@@ -849,7 +893,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   __shared__ __align__(16) uint8_t lds_k[2][Tile::kBytes];
   __shared__ __align__(16) uint8_t lds_v[2][Tile::kBytes];
   __shared__ __align__(16) float params[2][SCHEME == kKvRow ? 3 * KT : 4];
-  __shared__ __align__(16) int marks[2][KT];
+  __shared__ __align__(16) int marks[2][KT + 4];   // tile numbers: of a key with values that are not finite; [KT], of any row of zeros
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h2 = lane >> 5;
   const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
@@ -895,7 +939,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   auto is_edge = [&](int key, uint32_t held) {
     return key < v.all_begin || key + KT > v.all_end || held != (1u << (KT / 16)) - 1;
   };
-  if (threadIdx.x < KT) marks[0][threadIdx.x] = marks[1][threadIdx.x] = -1;
+  if (threadIdx.x <= KT) marks[0][threadIdx.x] = marks[1][threadIdx.x] = -1;
   __syncthreads();
   Tile next;
   uint32_t held = 0, held_next = 0;
@@ -903,7 +947,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
   auto put = [&](int x, int key) {   // the registers' tile x to LDS
     if (is_edge(key, held_next)) next.clean_v(marks[x & 1], x);
     next.store_k(lds_k[x & 1], k0);
-    next.store_v(lds_v[x & 1], v0, params[x & 1], ks0);
+    next.store_v(g, lds_v[x & 1], v0, params[x & 1], ks0, &marks[x & 1][KT], x);
   };
   auto get = [&](int key) {          // the tile at `key` to the registers, and the pages of the one behind it
     next.load(g, hk, key);
@@ -994,6 +1038,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArg
     const float base = m == -INFINITY ? 0.0f : m - weight_shift<SCHEME>();
     uint4 wf[2 * NB];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    if (SCHEME == kKvRow && marks[buf][KT] == x) {
+      asm volatile("");   // a branch
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (pr[2 * KT + 32 * b + 8 * (r >> 2) + 4 * h2 + (r & 3)] == 0.0f)
+            sum[r & 3] += __builtin_amdgcn_exp2f(s[b][r] - kSmallestLog - base);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -1166,14 +1219,33 @@ struct Plan {
   int64_t tiles, parts;   // bounds, per head of the cache
 };
 
+template <int NQ>
+int stream_waves_of(const AttendArgs& g) {
+  const bool bf16 = g.scheme == kKvBf16;
+  switch (g.D) {
+    case 64: return bf16 ? stream_waves<kKvBf16, 64, NQ>() : stream_waves<kKvRow, 64, NQ>();
+    case 128: return bf16 ? stream_waves<kKvBf16, 128, NQ>() : stream_waves<kKvRow, 128, NQ>();
+    case 192: return bf16 ? stream_waves<kKvBf16, 192, NQ>() : stream_waves<kKvRow, 192, NQ>();
+    default: return bf16 ? stream_waves<kKvBf16, 256, NQ>() : stream_waves<kKvRow, 256, NQ>();
+  }
+}
+
 Plan plan_of(const AttendArgs& g) {
   const int64_t rows = g.T * (g.H / g.Hk), seqs = std::max<int64_t>(1, std::min<int64_t>(g.B, g.T));
   const int64_t mean = (rows + seqs - 1) / seqs;
   Plan p;
   p.bm = mean <= 16 ? 16 : mean <= 32 ? 32 : 128;
   p.tiles = rows / p.bm + seqs;
-  p.target = p.bm == 128 ? 512 : 1024;
-  p.min_chunk = p.bm == 128 ? 16 : 4;
+  if (p.bm == 128) {
+    p.target = 512;
+    p.min_chunk = 16;
+  } else {
+    // One round of the workgroups that fit on the card where few row tiles share it, three where ranges of many
+    // sequences have to even out.
+    const int fit = 256 * (p.bm == 16 ? stream_waves_of<1>(g) : stream_waves_of<2>(g));
+    p.target = std::max(rows / p.bm, seqs) * g.Hk * 4 <= fit ? fit : 3 * fit;
+    p.min_chunk = 4;
+  }
   const int64_t key_tiles = ((g.width << g.page_shift) + kKeyTile - 1) / kKeyTile;
   p.parts = 0;
   if (key_tiles <= p.min_chunk) p.target = 0;
@@ -1219,13 +1291,13 @@ size_t kv_attention_ws_bytes(const AttendArgs& g) {
   return (size_t)p.parts * g.Hk * p.bm * (g.D + 4) * 4;
 }
 
-hipError_t launch_kv_attention(int scheme, AttendArgs g, hipStream_t st) {
+hipError_t launch_kv_attention(AttendArgs g, hipStream_t st) {
   const Plan p = plan_of(g);
   g.target = p.target;
   g.min_chunk = p.min_chunk;
   g.parts = (int)p.parts;
-  if (scheme == kKvBf16) return attend_as<kKvBf16>(g, p, st);
-  return scheme == kKvTensor ? attend_as<kKvTensor>(g, p, st) : attend_as<kKvRow>(g, p, st);
+  if (g.scheme == kKvBf16) return attend_as<kKvBf16>(g, p, st);
+  return g.scheme == kKvTensor ? attend_as<kKvTensor>(g, p, st) : attend_as<kKvRow>(g, p, st);
 }
 
 const char* kv_attention_kernel_name(const AttendArgs& g) {

@@ -246,7 +246,7 @@ struct AttendArgs {
   int64_t ldqt, ldqh, T;
   const void *k_codes, *v_codes;
   const float *k_scales, *v_scales;
-  int n_pages, page_shift, H, Hk, D;
+  int scheme, n_pages, page_shift, H, Hk, D;
   const int32_t *starts, *lens, *pages;
   int B;
   int64_t width, ldp;
@@ -258,10 +258,10 @@ struct AttendArgs {
   float* ws;
   int target, min_chunk, parts;   // set by the launcher: ranges in all, least key tiles of one, places per head
 };
-// These go by T, H, Hk, D, B, width and page_shift alone.
+// These go by scheme, T, H, Hk, D, B, width and page_shift alone.
 bool kv_attention_fits(const AttendArgs& g);
 size_t kv_attention_ws_bytes(const AttendArgs& g);
 const char* kv_attention_kernel_name(const AttendArgs& g);
-hipError_t launch_kv_attention(int scheme, AttendArgs g, hipStream_t st);
+hipError_t launch_kv_attention(AttendArgs g, hipStream_t st);
 
 }  // namespace pql

@@ -450,6 +450,26 @@ def test_long_contexts(scheme, new, seqs):
     run_case(12, scheme, seqs, new, 4, 1, 64, 64)
 
 
+@pytest.mark.parametrize("scheme", ["fp8_row", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("sizes", [(1e-6, 0.0), (1e-20, 0.0), (1e6, 1.0), (1e-8, 1.0), (1e30, 1e20), (1e-24, 1e-24)])
+def test_value_sizes(scheme, new, sizes):
+    """Tokens whose values are of very different sizes, rows of zeros (their scale is 1) among small ones, and a
+    scale of exactly 1 that is none."""
+    rng = np.random.default_rng(14)
+    L, Hk, D = 300, 2, 128
+    x = [rng.standard_normal((L, Hk, D)) for _ in "kv"]
+    x[1] *= rng.choice(sizes, (L, Hk, 1))
+    x[1][5] = 0.0
+    x[1][L - new, :, 0], x[1][L - new, :, 1:] = 448.0 * (sizes[0] < 1e10), 0.0
+    bits = [[bf16_bits(a) for a in x]]
+    fill = Filled(rng, scheme, [L], Hk, D, 16, [new], bits=bits)
+    qb = bf16_bits(rng.standard_normal((new, 4, D)) * 2)
+    q64 = F.bf16_to_f32(qb).astype(np.float64)
+    got, lse = pql.kv_attention(up16(qb), fill.cache, fill.starts, fill.lens, fill.pages, return_lse=True)
+    check_attention(fill, q64, f64(got), f64(lse), expected(fill, q64), small=L)
+
+
 # ---------------------------------------------------------------- together
 def layer(x, cache, batch, table, H, Hk, D):
     """One layer's attention from its projection x [T, (H + 2 Hk) D]."""

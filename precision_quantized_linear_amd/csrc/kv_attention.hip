@@ -306,6 +306,21 @@ __device__ __forceinline__ void value_scale(float vs, float& lv, float& rv) {
   rv = __builtin_amdgcn_rcpf(vs);
 }
 
+// Lanes 0 .. 7 of each row of 16 lanes, in all of the row's lanes.
+__device__ __forceinline__ void row_lanes8(float x, float (&out)[8]) {
+#define PQL_ROW_LANE(n) \
+  out[n] = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + n, 0xF, 0xF, true))
+  PQL_ROW_LANE(0);
+  PQL_ROW_LANE(1);
+  PQL_ROW_LANE(2);
+  PQL_ROW_LANE(3);
+  PQL_ROW_LANE(4);
+  PQL_ROW_LANE(5);
+  PQL_ROW_LANE(6);
+  PQL_ROW_LANE(7);
+#undef PQL_ROW_LANE
+}
+
 // The second products' operands, as 16-byte words.
 template <int SCHEME>
 __device__ __forceinline__ v4f mfma16_pv(uint4 v, uint4 w, v4f acc) {
@@ -379,7 +394,7 @@ struct StreamTile {
   static constexpr int VW = D / 16 * EB / 4;                 // words of a lane per key
   uint4 k[2][KW];
   uint32_t v[8][VW];
-  float4 ks[2], vs[2];
+  float ks, vs;                                              // of key 16 (c / 4 % 2) + 4 q + c % 4
   int64_t row[2];
   bool held[2], next_held[2];
 
@@ -394,7 +409,6 @@ struct StreamTile {
       const uint8_t* p = static_cast<const uint8_t*>(g.k_codes) + row[t] * (D * EB) + (c * (D * EB) + q * (D / 4 * EB));
 #pragma unroll
       for (int i = 0; i < KW; ++i) k[t][i] = ldg16(p + 16 * i);
-      if constexpr (SCHEME == kKvRow) ks[t] = *reinterpret_cast<const float4*>(g.k_scales + row[t] + 4 * q);
     }
   }
   __device__ __forceinline__ void load_v(const AttendArgs& g, int lane) {
@@ -411,10 +425,11 @@ struct StreamTile {
       }
     }
   }
-  __device__ __forceinline__ void load_vs(const AttendArgs& g, int lane) {
+  __device__ __forceinline__ void load_scales(const AttendArgs& g, int lane) {
     if constexpr (SCHEME == kKvRow) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) vs[t] = *reinterpret_cast<const float4*>(g.v_scales + row[t] + 4 * (lane >> 4));
+      const int64_t r = ((lane & 4) ? row[1] : row[0]) + (4 * (lane >> 4) + (lane & 3));
+      ks = g.k_scales[r];
+      vs = g.v_scales[r];
     }
   }
 };
@@ -446,7 +461,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
   if (key < key_last) {
     x.find(g, w.b, hk, key);
     x.load_k(g, lane);
-    x.load_vs(g, lane);
+    x.load_scales(g, lane);
     x.load_v(g, lane);
   }
 
@@ -508,22 +523,23 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
         for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[n][i];
     }
     float rv[8];
-    uint32_t ones = 0;      // keys whose value scale is 1, then those whose values are all zero
+    uint32_t zero_rows = 0;   // keys whose values are all zero, found where a scale is 1 (its logarithm 0)
+    bool zeros = false;
     if constexpr (SCHEME == kKvRow) {
+      // every lane prepares one of the eight keys that its row of 16 lanes has, and they read each other's
+      const float k1 = x.ks * ks0;
+      float l1, r1;
+      value_scale(x.vs, l1, r1);
+      float kk[8], lv[8];
+      row_lanes8(k1, kk);
+      row_lanes8(l1, lv);
+      row_lanes8(r1, rv);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float k4[4] = {x.ks[t].x, x.ks[t].y, x.ks[t].z, x.ks[t].w};
-        const float v4[4] = {x.vs[t].x, x.vs[t].y, x.vs[t].z, x.vs[t].w};
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ones |= (uint32_t)(v4[i] == 1.0f) << (4 * t + i);
-          float lv;
-          value_scale(v4[i], lv, rv[4 * t + i]);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) s[n][4 * t + i] = __builtin_fmaf(s[n][4 * t + i], k4[i] * ks0, lv);
-        }
-      }
-      if (__any(ones)) {
+        for (int i = 0; i < 8; ++i) s[n][i] = __builtin_fmaf(s[n][i], kk[i], lv[i]);
+      zeros = __any(l1 == 0.0f);
+      if (zeros) {
         asm volatile("");   // a branch
         uint32_t some = 0;
 #pragma unroll
@@ -532,12 +548,13 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
           for (int j = 0; j < VW; ++j) some |= magnitude(x.v[i][j]) ? 1u << i : 0u;
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) some |= __shfl_xor(some, d);
-        ones &= ~some;      // rows of zeros; the logarithm of 1 is 0
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (ones >> i & 1) rv[i] = 0.0f;
+          const bool zero = rv[i] == 1.0f && !(some >> i & 1);
+          zero_rows |= (uint32_t)zero << i;
+          if (zero) rv[i] = 0.0f;
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) s[n][i] += ones >> i & 1 ? kSmallestLog : 0.0f;
+          for (int n = 0; n < NQ; ++n) s[n][i] += zero ? kSmallestLog : 0.0f;
         }
       }
     } else {
@@ -549,7 +566,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
     // the next step's keys come into the registers of this one's, which are done with
     if (more) {
       x.load_k(g, lane);
-      x.load_vs(g, lane);
+      x.load_scales(g, lane);
     }
     // Keys that some rows do not see: their scores go, and values that are not finite are taken out of the
     // product (0 times them is not 0) and make the scores of rows that do see them NaN.
@@ -598,11 +615,11 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n] - weight_shift<SCHEME>();
       if constexpr (SCHEME == kKvRow) {
-        if (__any(ones)) {
+        if (zeros) {
           asm volatile("");   // a branch
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (ones >> i & 1) l[n] += __builtin_amdgcn_exp2f(s[n][i] - kSmallestLog - base);
+            if (zero_rows >> i & 1) l[n] += __builtin_amdgcn_exp2f(s[n][i] - kSmallestLog - base);
         }
       }
       float e[8];

@@ -1253,14 +1253,19 @@ Plan plan_of(const AttendArgs& g) {
   Plan p;
   p.bm = mean <= 16 ? 16 : mean <= 32 ? 32 : 128;
   p.tiles = rows / p.bm + seqs;
+  // Ranges in rounds of the workgroups that fit on the card: each row tile's last range is half a range short
+  // on average, so that `target` full ones make target + tiles / 2.  Many rows: as few rounds as leave half of
+  // the last one's ranges full.  Few rows: one round where few row tiles share the card, three where
+  // ranges of many sequences have to even out.
+  const int64_t all = std::max((rows + p.bm - 1) / p.bm, seqs) * g.Hk;   // row tiles, at least
   if (p.bm == 128) {
-    p.target = 512;
+    constexpr int fit = 512;
+    const int64_t rounds = (all / 2 + fit / 2 + fit - 1) / fit;
+    p.target = (int)(rounds * fit - all / 2);
     p.min_chunk = 16;
   } else {
-    // One round of the workgroups that fit on the card where few row tiles share it, three where ranges of many
-    // sequences have to even out.
     const int fit = 256 * (p.bm == 16 ? stream_waves_of<1>(g) : stream_waves_of<2>(g));
-    p.target = std::max(rows / p.bm, seqs) * g.Hk * 4 <= fit ? fit : 3 * fit;
+    p.target = all * 4 <= fit ? fit - (int)all / 2 : (int)std::max<int64_t>(fit, 3 * fit - all / 2);
     p.min_chunk = 4;
   }
   const int64_t key_tiles = ((g.width << g.page_shift) + kKeyTile - 1) / kKeyTile;
@@ -1281,7 +1286,8 @@ hipError_t attend_with(AttendArgs& g, const Plan& p, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.target == 0) return e;
   const unsigned joins = (unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk);
-  if (p.bm == 128) hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D, 4>), dim3(joins, 32), dim3(256), 0, st, g);
+  constexpr int kRows = D <= 128 ? 16 : 8;
+  if (p.bm == 128) hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D, kRows>), dim3(joins, 128 / kRows), dim3(256), 0, st, g);
   else if (joins < 64 && p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D, 1>), dim3(joins, 16), dim3(256), 0, st, g);
   else if (p.bm == 16) hipLaunchKernelGGL((k_attend_join<SCHEME, 16, D, 4>), dim3(joins, 4), dim3(256), 0, st, g);
   else if (joins < 64) hipLaunchKernelGGL((k_attend_join<SCHEME, 32, D, 1>), dim3(joins, 32), dim3(256), 0, st, g);

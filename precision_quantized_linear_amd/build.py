@@ -44,7 +44,9 @@ def compile_flags():
 # AGPRs) spares one v_accvgpr_read per element.
 EXTRA_FLAGS = {"gemm_block.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "gemm_block256.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "moe_gemm_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "moe_gemm_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               # the attention rescales its sums on the vector units, which cannot reach AGPRs
+               "kv_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

@@ -904,7 +904,7 @@ struct KeyTile {
 };
 
 template <int SCHEME, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attend_tile(AttendArgs g) {
+__global__ __launch_bounds__(256, D <= 192 ? 2 : 1) void k_attend_tile(AttendArgs g) {
   typedef KeyTile<SCHEME, D> Tile;
   constexpr int BM = 128, KT = Tile::KT, NB = KT / 32, ND = D / 32;
   __shared__ __align__(16) uint8_t lds_k[2][Tile::kBytes];

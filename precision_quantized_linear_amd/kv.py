@@ -298,18 +298,19 @@ def kv_read(cache: KVCache, slots: torch.Tensor, out=None):
     device, n = slots.device, slots.numel()
     _check_vector(slots, "slots", torch.int32, n, device)
     _check_cache(cache, device)
-    shape = (n, cache.n_kv_heads, cache.head_dim)
+    H, D = cache.n_kv_heads, cache.head_dim
     if out is None:
-        out = [torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in "kv"]
-    k, v = out
-    *ks, kt, kh = _heads(k, "k out", device)
-    *vs, vt, vh = _heads(v, "v out", device)
-    if tuple(ks) != shape or tuple(vs) != shape:
-        raise ValueError(f"out must be two tensors of {shape}")
+        k, v = (torch.empty((n, H, D), dtype=torch.bfloat16, device=device) for _ in "kv")
+        kt, kh, vt, vh = H * D, D, H * D, D
+    else:
+        k, v = out
+        *ks, kt, kh = _heads(k, "k out", device)
+        *vs, vt, vh = _heads(v, "v out", device)
+        if ks != [n, H, D] or vs != [n, H, D]:
+            raise ValueError(f"out must be two tensors of {(n, H, D)}")
     _on_device(device)
     _call(lib().pql_kv_read, "kv_read", device, KV_SCHEMES[cache.scheme], *_cache_args(cache), cache.n_pages,
-          cache.page_size, cache.n_kv_heads, cache.head_dim, slots.data_ptr(), n, k.data_ptr(), kt, kh, v.data_ptr(), vt,
-          vh)
+          cache.page_size, H, D, slots.data_ptr(), n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
     return k, v
 
 

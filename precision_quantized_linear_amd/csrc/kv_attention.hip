@@ -38,7 +38,8 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRise = 8.0f;       // m follows the maximum when that is so much higher
-constexpr float kSmallestValueScale = 0x1p-100f, kSmallestLog = -100.0f;
+// l is at most 2^(90 + 15) times the number of keys.
+constexpr float kSmallestValueScale = 0x1p-90f, kSmallestLog = -90.0f;
 
 template <int SCHEME>
 constexpr float weight_shift() { return SCHEME == kKvBf16 ? 0.0f : 7.0f; }
@@ -66,9 +67,10 @@ __device__ __forceinline__ uint32_t scan_add(uint32_t v) {   // inclusive
   v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, true);   // row 1's last lane to rows 2 and 3
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#define PQL_ADD_DPP(ctrl, rows) \
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xF, true))
+__device__ __forceinline__ double wave_sum(double v) {
+#define PQL_ADD_DPP(ctrl, rows)                                                                      \
+  v += __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), ctrl, rows, 0xF, true),    \
+                        __builtin_amdgcn_update_dpp(0, __double2loint(v), ctrl, rows, 0xF, true))
   PQL_ADD_DPP(0x111, 0xF);
   PQL_ADD_DPP(0x112, 0xF);
   PQL_ADD_DPP(0x114, 0xF);
@@ -76,7 +78,7 @@ __device__ __forceinline__ float wave_sum(float v) {
   PQL_ADD_DPP(0x142, 0xA);
   PQL_ADD_DPP(0x143, 0xC);
 #undef PQL_ADD_DPP
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63), __builtin_amdgcn_readlane(__double2loint(v), 63));
 }
 
 __device__ __forceinline__ int splits_of(int kt, int chunk) { return kt <= chunk ? 1 : (kt + chunk - 1) / chunk; }
@@ -104,15 +106,14 @@ struct Shapes {
       kt[r] = std::max(0, (end + kKeyTile - 1) / kKeyTile - begin / kKeyTile);
     }
   }
-  __device__ __forceinline__ float work() const {
-    return ((float)qt[0] * (float)kt[0] + (float)qt[1] * (float)kt[1]) +
-           ((float)qt[2] * (float)kt[2] + (float)qt[3] * (float)kt[3]);
+  // Whole numbers that fp64 holds exactly: every kernel gets the same sum, however its compiler fuses.
+  __device__ __forceinline__ double work() const {
+    return ((double)qt[0] * kt[0] + (double)qt[1] * kt[1]) + ((double)qt[2] * kt[2] + (double)qt[3] * kt[3]);
   }
 };
 
 // The range with number `idx` among a head's; with MULTI, of the row tiles of sequences that are cut, the
-// tile with number idx.  The chunk comes out of the same sums in the same order in every workgroup
-// and in k_attend_join.
+// tile with number idx.  The chunk is the same in every workgroup and in k_attend_join.
 template <int BM, bool MULTI>
 __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Work& w) {
   const int lane = threadIdx.x & 63;
@@ -120,14 +121,14 @@ __device__ __forceinline__ bool find_work(const AttendArgs& g, uint32_t idx, Wor
   x.load(g, 0);
   int chunk = INT32_MAX;
   if (g.target) {
-    float total = x.work();
+    double total = x.work();
     for (int b0 = 256; b0 < g.B; b0 += 256) {
       x.load(g, b0);
       total += x.work();
     }
     if (g.B > 256) x.load(g, 0);
-    const float want = __builtin_ceilf(wave_sum(total) * (float)g.Hk / (float)g.target);
-    chunk = std::max(g.min_chunk, (int)fminf(want, 1073741824.0f));
+    const double want = __builtin_ceil(wave_sum(total) * (double)g.Hk / (double)g.target);
+    chunk = std::max(g.min_chunk, (int)fmin(want, 1073741824.0));
     chunk = __builtin_amdgcn_readfirstlane(chunk);
   }
   uint32_t before = 0, parts_before = 0;
@@ -1228,8 +1229,18 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
 }
 
 // ---------------------------------------------------------------- choice and launch
-// Rows per tile by the mean rows of a sequence's head; at most `target` ranges where contexts are worth
-// cutting.
+// The choices, by what the host knows (sizes, not lengths).  us, codes with a scale per token, G = 4, Hk = 8.
+//
+// Rows per tile by the mean rows of a sequence's head.  The three kernels at 128 head values
+// (16 | 32 | 128 rows per tile):
+//   32 sequences over 8192, rows 16: 79 | 86 | 125, 32: 90 | 90 | 127, 48: 99 | 100 | 138, 64: 114 | 114 | 138,
+//   128: 175 | 149 | 147;   8 sequences, 64: 44 | 35 | 46, 128: 71 | 65 | 51, 256: 110 | 99 | 64;
+//   1 over 16384, 64: 29 | 26 | 41, 128: 40 | 35 | 44, 256: 63 | 49 | 48.
+// 64 values are alike (8 sequences, 64: 29 | 29 | 36, 128: 53 | 44 | 40).  At 192 and 256 values the many-row
+// kernel has half the waves or half the key tile (256 values, 8 sequences, 64 rows: 78 | 81 | 141, 128:
+// 124 | 113 | 149, 256: 203 | 174 | 199), so that few rows reach further there; up to 128 rows, because many
+// short contexts, which the host can not tell, want tiles of 128 earlier (32 of 600 tokens, bf16, 128 rows: 86 |
+// 81 | 62).
 struct Plan {
   int bm;
   int target, min_chunk;
@@ -1251,18 +1262,23 @@ Plan plan_of(const AttendArgs& g) {
   const int64_t rows = g.T * (g.H / g.Hk), seqs = std::max<int64_t>(1, std::min<int64_t>(g.B, g.T));
   const int64_t mean = (rows + seqs - 1) / seqs;
   Plan p;
-  p.bm = mean <= 16 ? 16 : mean <= 32 ? 32 : 128;
+  p.bm = mean <= (g.D <= 128 ? 32 : 64) ? 16 : mean <= (g.D <= 128 ? 64 : 128) ? 32 : 128;
   p.tiles = rows / p.bm + seqs;
   // Ranges in rounds of the workgroups that fit on the card: each row tile's last range is half a range short
   // on average, so that `target` full ones make target + tiles / 2.  Many rows: as few rounds as leave half of
-  // the last one's ranges full.  Few rows: one round where few row tiles share the card, three where
-  // ranges of many sequences have to even out.
+  // the last one's ranges full (five chunks of 300: 96 -> 76 us).  Few rows: one round where few row tiles share
+  // the card (one token over 131000, in ranges: 512: 64, 768: 63, 1024: 75), three where ranges of many
+  // sequences have to even out (64 sequences up to 16384, 768: 157, 1536: 134, 2304: 129).
+  //
+  // The shortest range, in key tiles: few rows 4 (one token over 6007 in 2: 13.0, 4: 12.5, 8: 14.6).  Many rows 16,
+  // or 8 where row tiles leave three quarters of the card idle (1 sequence over 16384, 128 rows of 64 values: 42 ->
+  // 30; 32 of 600 tokens, 256 rows, not cut at 16: 34, cut at 8: 47; at 256 values 8 is no better).
   const int64_t all = std::max((rows + p.bm - 1) / p.bm, seqs) * g.Hk;   // row tiles, at least
   if (p.bm == 128) {
     constexpr int fit = 512;
     const int64_t rounds = (all / 2 + fit / 2 + fit - 1) / fit;
     p.target = (int)(rounds * fit - all / 2);
-    p.min_chunk = 16;
+    p.min_chunk = 4 * all <= fit && g.D <= 192 ? 8 : 16;
   } else {
     const int fit = 256 * (p.bm == 16 ? stream_waves_of<1>(g) : stream_waves_of<2>(g));
     p.target = all * 4 <= fit ? fit - (int)all / 2 : (int)std::max<int64_t>(fit, 3 * fit - all / 2);
@@ -1285,6 +1301,8 @@ hipError_t attend_with(AttendArgs& g, const Plan& p, hipStream_t st) {
   else hipLaunchKernelGGL((k_attend_tile<SCHEME, D>), grid, dim3(256), 0, st, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.target == 0) return e;
+  // Rows per workgroup of the join: 1 where there are few, for the most threads per row (one token over 60000, one
+  // head: 33 -> 19 us), else 4 (256 sequences over 4096: 277 -> 241 with 4).
   const unsigned joins = (unsigned)(std::min(p.tiles, p.parts / 2 + 1) * g.Hk);
   constexpr int kRows = D <= 128 ? 16 : 8;
   if (p.bm == 128) hipLaunchKernelGGL((k_attend_join<SCHEME, 128, D, kRows>), dim3(joins, 128 / kRows), dim3(256), 0, st, g);

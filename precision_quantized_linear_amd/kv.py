@@ -171,12 +171,16 @@ class KVCache:
         return self.k.device
 
 
-def kv_sizes(scheme: str, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int):
-    """(codes bytes, scales bytes) of each of a cache's two halves."""
+def _kv_scheme(scheme: str) -> int:
     if scheme not in KV_SCHEMES:
         raise ValueError(f"unknown cache scheme {scheme!r}; supported: {sorted(KV_SCHEMES)}")
+    return KV_SCHEMES[scheme]
+
+
+def kv_sizes(scheme: str, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int):
+    """(codes bytes, scales bytes) of each of a cache's two halves."""
     c, s = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().pql_kv_sizes(KV_SCHEMES[scheme], n_pages, page_size, n_kv_heads, head_dim, ctypes.byref(c),
+    _check(lib().pql_kv_sizes(_kv_scheme(scheme), n_pages, page_size, n_kv_heads, head_dim, ctypes.byref(c),
                               ctypes.byref(s)), "kv_sizes")
     return c.value, s.value
 
@@ -206,8 +210,7 @@ def kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, schem
 def _check_cache(c, device) -> None:
     if not isinstance(c, KVCache):
         raise ValueError("cache must be a KVCache")
-    if c.scheme not in KV_SCHEMES:
-        raise ValueError(f"unknown cache scheme {c.scheme!r}; supported: {sorted(KV_SCHEMES)}")
+    _kv_scheme(c.scheme)
     shape = (c.n_pages, c.n_kv_heads, c.page_size, c.head_dim)
     dtype = torch.bfloat16 if c.scheme == "bf16" else torch.uint8
     for t, name in ((c.k, "k"), (c.v, "v")):
@@ -320,14 +323,14 @@ def kv_attention_workspace(scheme: str, T: int, H: int, n_kv_heads: int, head_di
                            page_size: int) -> int:
     """Workspace bytes of a ``kv_attention`` call of these sizes (width: columns of its ``pages``)."""
     wsb = ctypes.c_size_t()
-    _check(lib().pql_kv_attention_workspace(KV_SCHEMES[scheme], T, H, n_kv_heads, head_dim, B, width, page_size,
+    _check(lib().pql_kv_attention_workspace(_kv_scheme(scheme), T, H, n_kv_heads, head_dim, B, width, page_size,
                                             ctypes.byref(wsb)), "kv_attention")
     return wsb.value
 
 
 def kv_kernel_name(scheme: str, T: int, H: int, n_kv_heads: int, head_dim: int, B: int, width: int,
                    page_size: int) -> str:
-    return lib().pql_kv_kernel_name(KV_SCHEMES[scheme], T, H, n_kv_heads, head_dim, B, width, page_size).decode()
+    return lib().pql_kv_kernel_name(_kv_scheme(scheme), T, H, n_kv_heads, head_dim, B, width, page_size).decode()
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, starts: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor, *,
@@ -341,7 +344,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, starts: torch.Tensor, lens: to
     at position i sees the tokens up to i (``causal``; otherwise all of its sequence) and, with
     ``window``, only the last ``window`` of those up to i.  H / n_kv_heads consecutive heads share a head
     of the cache.  ``scale``: on the products, head_dim^-0.5 by default.  Rows of no sequence are left as
-    they were in ``out``.  More: include/pql.h, pql_kv_attention."""
+    they were in ``out``.  ``workspace``: ``kv_attention_workspace`` bytes, not shared by calls that overlap
+    in time; allocated where it is not given.  More: include/pql.h, pql_kv_attention."""
     T, H, D, qt, qh = _heads(q, "q")
     device = q.device
     _check_cache(cache, device)

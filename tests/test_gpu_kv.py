@@ -270,7 +270,8 @@ def test_head_layouts(scheme, H, Hk):
 @pytest.mark.parametrize("scheme", SCHEMES)
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("new,seqs", [([5], [5]), ([100], [100]), ([64, 1, 130, 0, 33], [64, 500, 200, 77, 33]),
-                                      ([257], [700]), ([2, 2, 2], [2, 65, 129])])
+                                      ([257], [700]), ([2, 2, 2], [2, 65, 129]), ([20, 30], [700, 200]),
+                                      ([40, 39], [1500, 40])])
 def test_chunks(scheme, D, new, seqs):
     run_case(D + len(new), scheme, seqs, new, 4, 2, D, 16)
 
@@ -304,7 +305,7 @@ def test_far_scores(scheme, new):
 
 
 @pytest.mark.parametrize("scheme", SCHEMES)
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 70])
 def test_sees_nothing(scheme, new):
     """An empty sequence, more new tokens than the cache holds, sequences without pages: zeros and -inf."""
     fill, qb, got, lse = run_case(5, scheme, [0, 5, 200], [new, 9, new], 4, 2, 64, 16)
@@ -318,7 +319,7 @@ def test_sees_nothing(scheme, new):
 
 
 @pytest.mark.parametrize("scheme", SCHEMES)
-@pytest.mark.parametrize("new", [1, 50])
+@pytest.mark.parametrize("new", [1, 25, 50])
 @pytest.mark.parametrize("bad", [-1, 1 << 30, None])
 def test_absent_pages(scheme, new, bad):
     """Tokens on a page outside the cache take no part."""
@@ -333,7 +334,7 @@ def test_absent_pages(scheme, new, bad):
     check_attention(fill, q64, f64(got), f64(lse), expected(fill, q64, absent={0: gone}))
 
 
-@pytest.mark.parametrize("H,new", [(2, 1), (2, 6), (2, 50), (2, 200), (16, 3)])
+@pytest.mark.parametrize("H,new", [(2, 1), (2, 6), (2, 50), (2, 100), (2, 200), (16, 3)])
 @pytest.mark.parametrize("scheme,where", [(s, w) for s in SCHEMES for w in "kv"] + [("fp8_row", "scale")])
 def test_a_broken_token_reaches_only_those_that_see_it(scheme, H, new, where):
     """A NaN (or, in scales and bf16, an infinity) stored for one token: rows before it are exact, rows
@@ -366,13 +367,13 @@ def test_a_broken_token_reaches_only_those_that_see_it(scheme, H, new, where):
 
 
 @pytest.mark.parametrize("scheme", SCHEMES)
-@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("new", [1, 15, 30])
 def test_rows_of_no_sequence_and_strides(scheme, new):
     """Rows before the first and behind the last sequence, columns beside the heads: left as they were.
     q and out are parts of wider rows, pages a part of a wider table."""
     rng = np.random.default_rng(8)
     fill = Filled(rng, scheme, [120, 70], 2, 128, 16, [new, new + 1])
-    H, T = 6, fill.T + 7
+    H, T = 10, fill.T + 7
     qb = bf16_bits(rng.standard_normal((T, H, 128)))
     wide_q = torch.full((T, H * 128 + 40), 3.0, dtype=torch.bfloat16, device=DEV)
     q = wide_q[:, 16: 16 + H * 128].view(T, H, 128)
@@ -391,11 +392,12 @@ def test_rows_of_no_sequence_and_strides(scheme, new):
 
 
 @pytest.mark.parametrize("scheme", SCHEMES)
-def test_wild_batches_stay_inside(scheme):
+@pytest.mark.parametrize("new", [5, 30, 60])
+def test_wild_batches_stay_inside(scheme, new):
     """Starts, lengths and pages outside their ranges: nothing outside out, no fault, rows of a sound
     sequence beside them exact."""
     rng = np.random.default_rng(9)
-    fill = Filled(rng, scheme, [150] * 4, 2, 64, 16, [5] * 4)
+    fill = Filled(rng, scheme, [150] * 4, 2, 64, 16, [new] * 4)
     q = up16(bf16_bits(rng.standard_normal((fill.T, 4, 64))))
     for _ in range(8):
         starts = rng.integers(-(1 << 31), 1 << 31, 5).astype(np.int32)
@@ -408,7 +410,7 @@ def test_wild_batches_stay_inside(scheme):
             pql.kv_attention(q, fill.cache, s, l, p, out=buf[4: 4 + fill.T])
             edge = down(buf)
             assert (edge[:4] == SENTINEL).all() and (edge[-4:] == SENTINEL).all()
-    overlapping = dev(np.array([0, 20, 0, 20, 0], np.int32))      # every sequence claims every row
+    overlapping = dev(np.array([0, fill.T, 0, fill.T, 0], np.int32))      # every sequence claims every row
     pql.kv_attention(q, fill.cache, overlapping, fill.lens, fill.pages)
     torch.cuda.synchronize()
 
@@ -445,13 +447,14 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("scheme", SCHEMES)
-@pytest.mark.parametrize("new,seqs", [([1], [20000]), ([1] * 3, [9000, 5, 300]), ([2, 70], [6000, 3000])])
+@pytest.mark.parametrize("new,seqs", [([1], [20000]), ([1] * 3, [9000, 5, 300]), ([2, 70], [6000, 3000]), ([15] * 2, [4000, 9000]),
+                                      ([30] * 3, [4000, 200, 70])])
 def test_long_contexts(scheme, new, seqs):
     run_case(12, scheme, seqs, new, 4, 1, 64, 64)
 
 
 @pytest.mark.parametrize("scheme", ["fp8_row", "bf16"])
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 20, 40])
 @pytest.mark.parametrize("sizes", [(1e-6, 0.0), (1e-20, 0.0), (1e6, 1.0), (1e-8, 1.0), (1e30, 1e20), (1e-24, 1e-24)])
 def test_value_sizes(scheme, new, sizes):
     """Tokens whose values are of very different sizes, rows of zeros (their scale is 1) among small ones, and a
@@ -468,6 +471,52 @@ def test_value_sizes(scheme, new, sizes):
     q64 = F.bf16_to_f32(qb).astype(np.float64)
     got, lse = pql.kv_attention(up16(qb), fill.cache, fill.starts, fill.lens, fill.pages, return_lse=True)
     check_attention(fill, q64, f64(got), f64(lse), expected(fill, q64), small=L)
+
+
+@pytest.mark.parametrize("scheme,n_pages", [("bf16", 80000), ("fp8_row", 150000), ("fp8_tensor", 150000)])
+def test_past_32_bit_offsets(scheme, n_pages):
+    """A cache of more than 2^32 bytes a half, its last pages in use: written, read, attended over by both kernels."""
+    rng = np.random.default_rng(15)
+    Hk, D, ps, L = 4, 128, 64, 200
+    cache = pql.kv_cache(n_pages, ps, Hk, D, scheme, device=DEV,
+                         **(dict(k_scale=0.01, v_scale=0.02) if scheme == "fp8_tensor" else {}))
+    assert cache.k.numel() * cache.k.element_size() > 1 << 32
+    pages = np.arange(n_pages - 4, n_pages, dtype=np.int32)[None, ::-1].copy()
+    kb, vb = (bf16_bits(rng.standard_normal((L, Hk, D))) for _ in "kv")
+    starts, lens = dev(np.array([0, L], np.int32)), dev(np.array([L], np.int32))
+    slots, _ = pql.kv_slots(starts, lens, dev(pages), ps, L)
+    pql.kv_append(up16(kb), up16(vb), cache, slots)
+    small = Filled(rng, scheme, [L], Hk, D, ps, [L], bits=[[kb, vb]])
+    k, v = pql.kv_read(cache, slots)
+    ks, vs = pql.kv_read(small.cache, dev(okv.slots([0, L], [L], small.pages_np, ps, L)[0]))
+    assert torch.equal(k, ks) and torch.equal(v, vs)
+    for new in (L, 2):
+        qb = bf16_bits(rng.standard_normal((new, 8, D)))
+        starts = dev(np.array([0, new], np.int32))
+        got = pql.kv_attention(up16(qb), cache, starts, lens, dev(pages))
+        assert torch.equal(got, pql.kv_attention(up16(qb), small.cache, starts, lens, small.pages))
+
+
+@pytest.mark.parametrize("scheme", SCHEMES)
+@pytest.mark.parametrize("new", [1, 30, 60])
+def test_a_workspace_of_the_callers_and_broken_queries(scheme, new):
+    """Any bits in the workspace; a NaN or an infinity in one row of q reaches that row alone."""
+    rng = np.random.default_rng(16)
+    fill = Filled(rng, scheme, [3000, 1500], 2, 128, 16, [new, new])
+    qb = bf16_bits(rng.standard_normal((fill.T, 4, 128)))
+    q = up16(qb)
+    need = pql.kv_attention_workspace(scheme, fill.T, 4, 2, 128, 2, fill.pages.shape[1], 16)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    want = pql.kv_attention(q, fill.cache, fill.starts, fill.lens, fill.pages)
+    assert torch.equal(want, pql.kv_attention(q, fill.cache, fill.starts, fill.lens, fill.pages, workspace=ws))
+    with pytest.raises(ValueError):
+        pql.kv_attention(q, fill.cache, fill.starts, fill.lens, fill.pages, workspace=ws[:-1])
+    q[new, 1, 7], q[0, 2, 9] = float("nan"), float("inf")
+    got = pql.kv_attention(q, fill.cache, fill.starts, fill.lens, fill.pages, workspace=ws)
+    assert torch.isnan(got[new, 1]).all() and torch.isnan(got[0, 2]).all()
+    got[new, 1], got[0, 2] = want[new, 1], want[0, 2]
+    assert torch.equal(got, want)
 
 
 # ---------------------------------------------------------------- together

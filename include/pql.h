@@ -458,7 +458,7 @@ typedef enum pql_rope_layout { PQL_ROPE_HALF = 0, PQL_ROPE_INTERLEAVED = 1 } pql
  * the others copied.  freqs: device fp64 [rotary / 2]; the angle is formed and
  * reduced in fp64, so positions far out keep theirs, the rest is fp32 with one
  * rounding to bf16.  out may be x itself with the same strides (no other
- * overlap).  rotary: a multiple of 16 up to D, D a multiple of 8 up to 1024;
+ * overlap).  rotary: a multiple of 16 up to D, D a multiple of 8, 16 to 1024;
  * positions int32.  T = 0 is a no-op. */
 pql_status pql_rope(int layout, const void* x, int64_t T, int64_t H, int64_t D, int64_t ldxt, int64_t ldxh,
                     const int32_t* positions, const double* freqs, int64_t rotary, float scale, void* out,
@@ -512,7 +512,7 @@ pql_status pql_kv_attention_workspace(int scheme, int64_t T, int64_t H, int64_t 
  * matrix cores in 16 bits (fp16 for FP8 caches, bf16 for KV_BF16), one rounding to bf16 at
  * the end.  lse (fp32 [T, H], contiguous, or NULL) receives log sum_j exp(scale q . k_j).
  * A token that sees nothing gets zeros and an lse of -inf.  Rows of no sequence
- * are left as they were.  A NaN or an infinity in the cache reaches only
+ * are left as they were.  out and q do not overlap.  A NaN or an infinity in the cache reaches only
  * the tokens that see it, possibly all of their D values.  KV_FP8_ROW: value
  * scales below 2^-90 count as 2^-90, and a token's weight is lost beside one
  * whose value scale is 2^100 times its own.  Calls that overlap in time need

@@ -344,8 +344,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, starts: torch.Tensor, lens: to
     at position i sees the tokens up to i (``causal``; otherwise all of its sequence) and, with
     ``window``, only the last ``window`` of those up to i.  H / n_kv_heads consecutive heads share a head
     of the cache.  ``scale``: on the products, head_dim^-0.5 by default.  Rows of no sequence are left as
-    they were in ``out`` (which does not overlap q), or hold anything where it is not given.  ``workspace``: ``kv_attention_workspace`` bytes, not shared by calls that overlap
-    in time; allocated where it is not given.  More: include/pql.h, pql_kv_attention."""
+    they were in ``out`` (which does not overlap q), or hold anything where it is not given.
+    ``workspace``: ``kv_attention_workspace`` bytes, not shared by calls that overlap in time; allocated
+    where it is not given.  More: include/pql.h, pql_kv_attention."""
     T, H, D, qt, qh = _heads(q, "q")
     device = q.device
     _check_cache(cache, device)

@@ -38,7 +38,9 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRise = 8.0f;       // m follows the maximum when that is so much higher
-// l is at most 2^(90 + 15) times the number of keys.
+// l is at most 2^(90 + 15) times the number of keys.  Rows of zeros alone make it so large, at an m of -90; where
+// values with a scale of 2^36 or more join them, the factor between the two m is below fp32's range although
+// the rows of zeros still count, so l is multiplied by the factor's root twice.
 constexpr float kSmallestValueScale = 0x1p-90f, kSmallestLog = -90.0f;
 
 template <int SCHEME>
@@ -367,11 +369,11 @@ __device__ __forceinline__ void store_row(const AttendArgs& g, const Seq& s, int
   if (g.lse && d == 0) g.lse[t * g.H + h] = lse_of<SCHEME>(m, SCHEME == kKvBf16 ? le : l);
 }
 
-// What the sums of a range with maximum m count for beside the highest one.  A range that saw nothing but
-// NaN has no maximum; its sums are NaN and stay.
-__device__ __forceinline__ float join_factor(float m, float l, float top) {
+// The root of what the sums of a range with maximum m count for beside the highest one.  A range that saw
+// nothing but NaN has no maximum; its sums are NaN and stay.
+__device__ __forceinline__ float join_root(float m, float l, float top) {
   if (m == -INFINITY) return l != 0.0f ? 1.0f : 0.0f;
-  return __builtin_amdgcn_exp2f(m - top);
+  return __builtin_amdgcn_exp2f(0.5f * (m - top));
 }
 
 // Parts, [Hk, parts, BM, D] sums and then [Hk, parts, BM] x (m, l, l of weights as they were, unused), fp32.
@@ -614,9 +616,9 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       top = max32(max16(top));
       if (__any(top > m[n] + kRise)) {
         const float next = top > m[n] + kRise ? top : m[n];
-        const float a = next == m[n] ? 1.0f : __builtin_amdgcn_exp2f(m[n] - next);
+        const float h = next == m[n] ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (m[n] - next)), a = h * h;
         m[n] = next;
-        l[n] *= a;
+        l[n] = l[n] * h * h;
         le[n] *= a;
 #pragma unroll
         for (int j = 0; j < JD; ++j) o[n][j] *= a;
@@ -702,8 +704,8 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float f = join_factor(sm[x][r], sl[x][r], top);
-        sum = __builtin_fmaf(f, sl[x][r], sum);
+        const float h = join_root(sm[x][r], sl[x][r], top), f = h * h;
+        sum = __builtin_fmaf(h * sl[x][r], h, sum);
         exact = __builtin_fmaf(f, se[x][r], exact);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[x][r][8 * tr + e], acc[e]);
@@ -1060,9 +1062,9 @@ __global__ __launch_bounds__(256, D <= 192 ? 2 : 1) void k_attend_tile(AttendArg
     top = max32(top);
     if (__any(top > m + kRise)) {
       const float nm = top > m + kRise ? top : m;
-      const float a = nm == m ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+      const float h = nm == m ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (m - nm)), a = h * h;
       m = nm;
-      l *= a;
+      l = l * h * h;
       le *= a;
 #pragma unroll
       for (int j = 0; j < ND; ++j) o[j] *= a;
@@ -1198,17 +1200,17 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
       float next = top;
 #pragma unroll
       for (int u = 0; u < U; ++u) next = fmaxf(next, x0 + u * NG < mine ? p[u].x : -INFINITY);
-      const float old = join_factor(top, sum, next);
+      const float root = join_root(top, sum, next), old = root * root;
       top = next;
-      sum *= old;
+      sum = sum * root * root;
       exact *= old;
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (x0 + u * NG >= mine) break;
-        const float f = join_factor(p[u].x, p[u].y, top);
-        sum = __builtin_fmaf(f, p[u].y, sum);
+        const float h = join_root(p[u].x, p[u].y, top), f = h * h;
+        sum = __builtin_fmaf(h * p[u].y, h, sum);
         exact = __builtin_fmaf(f, p[u].z, exact);
         acc[0] = __builtin_fmaf(f, a[u].x, acc[0]);
         acc[1] = __builtin_fmaf(f, a[u].y, acc[1]);
@@ -1234,8 +1236,8 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
   for (int x = 0; x < NG; ++x) top = fmaxf(top, sm[ri][x]);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
   for (int x = 0; x < NG; ++x) {
-    const float f = join_factor(sm[ri][x], sl[ri][x], top);
-    sum = __builtin_fmaf(f, sl[ri][x], sum);
+    const float h = join_root(sm[ri][x], sl[ri][x], top), f = h * h;
+    sum = __builtin_fmaf(h * sl[ri][x], h, sum);
     exact = __builtin_fmaf(f, se[ri][x], exact);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[ri][x][8 * tr + e], acc[e]);

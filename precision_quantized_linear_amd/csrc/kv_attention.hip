@@ -309,6 +309,19 @@ __device__ __forceinline__ void value_scale(float vs, float& lv, float& rv) {
   rv = __builtin_amdgcn_rcpf(vs);
 }
 
+// 2^d, d <= 0, as a product: its root twice where rows of zeros can make l that large, so that l times both stays
+// in range where 2^d does not.
+struct Factor {
+  float a, b;
+  __device__ __forceinline__ float whole() const { return a * b; }
+};
+template <int SCHEME>
+__device__ __forceinline__ Factor factor_of(float d) {
+  if constexpr (SCHEME != kKvRow) return Factor{__builtin_amdgcn_exp2f(d), 1.0f};
+  const float root = __builtin_amdgcn_exp2f(0.5f * d);
+  return Factor{root, root};
+}
+
 // Lanes 0 .. 7 of each row of 16 lanes, in all of the row's lanes.
 __device__ __forceinline__ void row_lanes8(float x, float (&out)[8]) {
 #define PQL_ROW_LANE(n) \
@@ -369,11 +382,12 @@ __device__ __forceinline__ void store_row(const AttendArgs& g, const Seq& s, int
   if (g.lse && d == 0) g.lse[t * g.H + h] = lse_of<SCHEME>(m, SCHEME == kKvBf16 ? le : l);
 }
 
-// The root of what the sums of a range with maximum m count for beside the highest one.  A range that saw
-// nothing but NaN has no maximum; its sums are NaN and stay.
-__device__ __forceinline__ float join_root(float m, float l, float top) {
-  if (m == -INFINITY) return l != 0.0f ? 1.0f : 0.0f;
-  return __builtin_amdgcn_exp2f(0.5f * (m - top));
+// What the sums of a range with maximum m count for beside the highest one.  A range that saw nothing but
+// NaN has no maximum; its sums are NaN and stay.
+template <int SCHEME>
+__device__ __forceinline__ Factor join_factor(float m, float l, float top) {
+  if (m == -INFINITY) return l != 0.0f ? Factor{1.0f, 1.0f} : Factor{0.0f, 0.0f};
+  return factor_of<SCHEME>(m - top);
 }
 
 // Parts, [Hk, parts, BM, D] sums and then [Hk, parts, BM] x (m, l, l of weights as they were, unused), fp32.
@@ -616,9 +630,10 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       top = max32(max16(top));
       if (__any(top > m[n] + kRise)) {
         const float next = top > m[n] + kRise ? top : m[n];
-        const float h = next == m[n] ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (m[n] - next)), a = h * h;
+        const Factor f = next == m[n] ? Factor{1.0f, 1.0f} : factor_of<SCHEME>(m[n] - next);
+        const float a = f.whole();
         m[n] = next;
-        l[n] = l[n] * h * h;
+        l[n] = l[n] * f.a * f.b;
         le[n] *= a;
 #pragma unroll
         for (int j = 0; j < JD; ++j) o[n][j] *= a;
@@ -704,8 +719,9 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float h = join_root(sm[x][r], sl[x][r], top), f = h * h;
-        sum = __builtin_fmaf(h * sl[x][r], h, sum);
+        const Factor by = join_factor<SCHEME>(sm[x][r], sl[x][r], top);
+        const float f = by.whole();
+        sum = __builtin_fmaf(sl[x][r] * by.b, by.a, sum);
         exact = __builtin_fmaf(f, se[x][r], exact);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[x][r][8 * tr + e], acc[e]);
@@ -1062,9 +1078,10 @@ __global__ __launch_bounds__(256, D <= 192 ? 2 : 1) void k_attend_tile(AttendArg
     top = max32(top);
     if (__any(top > m + kRise)) {
       const float nm = top > m + kRise ? top : m;
-      const float h = nm == m ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (m - nm)), a = h * h;
+      const Factor f = nm == m ? Factor{1.0f, 1.0f} : factor_of<SCHEME>(m - nm);
+      const float a = f.whole();
       m = nm;
-      l = l * h * h;
+      l = l * f.a * f.b;
       le *= a;
 #pragma unroll
       for (int j = 0; j < ND; ++j) o[j] *= a;
@@ -1200,17 +1217,19 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
       float next = top;
 #pragma unroll
       for (int u = 0; u < U; ++u) next = fmaxf(next, x0 + u * NG < mine ? p[u].x : -INFINITY);
-      const float root = join_root(top, sum, next), old = root * root;
+      const Factor by = join_factor<SCHEME>(top, sum, next);
+      const float old = by.whole();
       top = next;
-      sum = sum * root * root;
+      sum = sum * by.b * by.a;
       exact *= old;
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (x0 + u * NG >= mine) break;
-        const float h = join_root(p[u].x, p[u].y, top), f = h * h;
-        sum = __builtin_fmaf(h * p[u].y, h, sum);
+        const Factor by = join_factor<SCHEME>(p[u].x, p[u].y, top);
+        const float f = by.whole();
+        sum = __builtin_fmaf(p[u].y * by.b, by.a, sum);
         exact = __builtin_fmaf(f, p[u].z, exact);
         acc[0] = __builtin_fmaf(f, a[u].x, acc[0]);
         acc[1] = __builtin_fmaf(f, a[u].y, acc[1]);
@@ -1236,8 +1255,9 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
   for (int x = 0; x < NG; ++x) top = fmaxf(top, sm[ri][x]);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.0f, exact = 0.0f;
   for (int x = 0; x < NG; ++x) {
-    const float h = join_root(sm[ri][x], sl[ri][x], top), f = h * h;
-    sum = __builtin_fmaf(h * sl[ri][x], h, sum);
+    const Factor by = join_factor<SCHEME>(sm[ri][x], sl[ri][x], top);
+    const float f = by.whole();
+    sum = __builtin_fmaf(sl[ri][x] * by.b, by.a, sum);
     exact = __builtin_fmaf(f, se[ri][x], exact);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f, so[ri][x][8 * tr + e], acc[e]);

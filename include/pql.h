@@ -514,10 +514,10 @@ pql_status pql_kv_attention_workspace(int scheme, int64_t T, int64_t H, int64_t 
  * A token that sees nothing gets zeros and an lse of -inf.  Rows of no sequence
  * are left as they were.  out and q do not overlap.  A NaN or an infinity in
  * the cache reaches only the tokens that see it, possibly all of their D values.
- * KV_FP8_ROW: value scales below 2^-90 count as 2^-90, and a token's weight is
- * lost beside one whose value scale is 2^100 times its own (never that of a token
- * whose values are all zero).  Calls that overlap in time need workspaces of
- * their own. */
+ * KV_FP8_ROW: values whose scale is below 2^-90 are exact to 2^-113 (a negative
+ * scale counts as 0), and a token's weight is lost beside one whose value scale is
+ * 2^100 times its own, unless its own is below 2^-90 or its values are all zero.
+ * Calls that overlap in time need workspaces of their own. */
 pql_status pql_kv_attention(int scheme, const void* q, int64_t ldqt, int64_t ldqh, int64_t T, int64_t H,
                             const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
                             int64_t n_pages, int64_t page_size, int64_t Hk, int64_t D, const int32_t* starts,

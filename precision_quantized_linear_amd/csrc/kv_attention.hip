@@ -38,10 +38,10 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRise = 8.0f;       // m follows the maximum when that is so much higher
-// l is at most 2^(90 + 15) times the number of keys.  Rows of zeros alone make it so large, at an m of -90; where
-// values with a scale of 2^36 or more join them, the factor between the two m is below fp32's range although
-// the rows of zeros still count, so l is multiplied by the factor's root twice.
-constexpr float kSmallestValueScale = 0x1p-90f, kSmallestLog = -90.0f;
+// l is at most 2^(90 + 15) times the number of keys.  Slight keys (below) make it so large by themselves, at an m of
+// -90; where values with a scale of 2^36 or more join them, the factor between the two m is below fp32's range
+// although the slight keys still count, so l is multiplied by the factor's root twice.
+constexpr float kSmallestValueScale = 0x1p-90f, kSmallestLog = -90.0f, kNoShare = -200.0f;
 
 template <int SCHEME>
 constexpr float weight_shift() { return SCHEME == kKvBf16 ? 0.0f : 7.0f; }
@@ -299,17 +299,24 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t codes) { return codes & 0
 template <int SCHEME>
 __device__ __forceinline__ bool bad_word(uint32_t c) { return SCHEME == kKvBf16 ? bad_bf16(c) : bad_codes(c); }
 
-// A value scale as the weights take it: its logarithm and its reciprocal.  Callers look for rows of zeros where a
-// scale is 1: the quantizer's rule gives them that, which says nothing about their size and would lift m above all
-// weights that matter where the others' values are small.  Such a key has no weight (its logarithm is the
-// smallest scale's, its reciprocal 0) and adds 2^(s - m) to l by itself.
+// A value scale as the weights take it: its logarithm and its reciprocal.  Slight keys, looked for only where a scale
+// is 1 or below 2^-90, are rows of zeros (their scale of 1, by the quantizer's rule, says nothing about their
+// size and would lift m above all weights that matter where the others' values are small) and keys whose scale's
+// reciprocal l could not hold.  They have the logarithm -90 in m's sense, add 2^(s - m) to l by themselves, and their
+// weight then goes down by share_log: the logarithm of what the scale is of 2^-90, kNoShare for zeros.  That stands
+// in the reciprocal's place and marks them, being below 0; what it adds to l, times the weight, is below
+// 2^-80 of what they have added.  Below about 2^-115 a scale leaves fp16's range, an error of 2^-113 at most in a
+// value.  A negative scale counts as 0.
 __device__ __forceinline__ void value_scale(float vs, float& lv, float& rv) {
   vs = vs < kSmallestValueScale ? kSmallestValueScale : vs;   // a NaN stays one
   lv = __builtin_amdgcn_logf(vs);
   rv = __builtin_amdgcn_rcpf(vs);
 }
+__device__ __forceinline__ float share_log(float vs) {
+  return fminf(fmaxf(__builtin_amdgcn_logf(fmaxf(vs * 0x1p90f, 0.0f)), kNoShare), -0x1p-22f);
+}
 
-// 2^d, d <= 0, as a product: its root twice where rows of zeros can make l that large, so that l times both stays
+// 2^d, d <= 0, as a product: its root twice where slight keys can make l that large, so that l times both stays
 // in range where 2^d does not.
 struct Factor {
   float a, b;
@@ -547,8 +554,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
         for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[n][i];
     }
     float rv[8];
-    uint32_t zero_rows = 0;   // keys whose values are all zero, found where a scale is 1 (its logarithm 0)
-    bool zeros = false;
+    bool slight = false;   // any such key
     if constexpr (SCHEME == kKvRow) {
       // every lane prepares one of the eight keys that its row of 16 lanes has, and they read each other's
       const float k1 = x.ks * ks0;
@@ -562,9 +568,10 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[n][i] = __builtin_fmaf(s[n][i], kk[i], lv[i]);
-      zeros = __any(l1 == 0.0f);
-      if (zeros) {
+      slight = __any(x.vs == 1.0f || x.vs < kSmallestValueScale);
+      if (slight) {
         asm volatile("");   // a branch
+        row_lanes8(x.vs < kSmallestValueScale ? share_log(x.vs) : r1, rv);
         uint32_t some = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -575,8 +582,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool zero = rv[i] == 1.0f && !(some >> i & 1);
-          zero_rows |= (uint32_t)zero << i;
-          if (zero) rv[i] = 0.0f;
+          if (zero) rv[i] = kNoShare;
 #pragma unroll
           for (int n = 0; n < NQ; ++n) s[n][i] += zero ? kSmallestLog : 0.0f;
         }
@@ -640,11 +646,14 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
       }
       const float base = m[n] == -INFINITY ? 0.0f : m[n] - weight_shift<SCHEME>();
       if constexpr (SCHEME == kKvRow) {
-        if (zeros) {
+        if (slight) {
           asm volatile("");   // a branch
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (zero_rows >> i & 1) l[n] += __builtin_amdgcn_exp2f(s[n][i] - kSmallestLog - base);
+            if (rv[i] < 0.0f) {
+              l[n] += __builtin_amdgcn_exp2f(s[n][i] - kSmallestLog - base);
+              s[n][i] += rv[i];
+            }
         }
       }
       float e[8];
@@ -888,7 +897,7 @@ struct KeyTile {
       }
     }
   }
-  __device__ __forceinline__ void store_v(const AttendArgs& g, uint8_t* vl, int v0, float* params, float ks0, int* zeros,
+  __device__ __forceinline__ void store_v(const AttendArgs& g, uint8_t* vl, int v0, float* params, float ks0, int* slight,
                                           int number) const {
     const int t = threadIdx.x;
 #pragma unroll
@@ -918,14 +927,18 @@ struct KeyTile {
       if (t < KT) {
         float lv, rv;
         value_scale(vs, lv, rv);
+        if (vs < kSmallestValueScale) {
+          rv = share_log(vs);
+          *slight = number;
+        }
         if (vs == 1.0f) {
           const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g.v_codes) + row * D);
           uint32_t some = 0;
           for (int i = 0; i < D / 16; ++i) some |= magnitude(p[i].x | p[i].y | p[i].z | p[i].w);
           if (!some) {
             lv = kSmallestLog;
-            rv = 0.0f;
-            *zeros = number;
+            rv = kNoShare;
+            *slight = number;
           }
         }
         params[t] = ks * ks0;
@@ -936,14 +949,19 @@ struct KeyTile {
   }
 };
 
+// Workgroups per CU.  192 values with a scale per token spill 12 registers at two, and one is slower still (4096 new
+// tokens over 8192, 16 heads: 763 | 871 us; 512 over 16384: 223 | 313); 64 values of FP8 need one register less for three.
 template <int SCHEME, int D>
-__global__ __launch_bounds__(256, D <= 192 ? 2 : 1) void k_attend_tile(AttendArgs g) {
+constexpr int tile_waves() { return D == 64 && SCHEME != kKvBf16 ? 3 : D <= 192 ? 2 : 1; }
+
+template <int SCHEME, int D>
+__global__ __launch_bounds__(256, (tile_waves<SCHEME, D>())) void k_attend_tile(AttendArgs g) {
   typedef KeyTile<SCHEME, D> Tile;
   constexpr int BM = 128, KT = Tile::KT, NB = KT / 32, ND = D / 32;
   __shared__ __align__(16) uint8_t lds_k[2][Tile::kBytes];
   __shared__ __align__(16) uint8_t lds_v[2][Tile::kBytes];
   __shared__ __align__(16) float params[2][SCHEME == kKvRow ? 3 * KT : 4];
-  __shared__ __align__(16) int marks[2][KT + 4];   // tile numbers: of a key with values that are not finite; [KT], of any row of zeros
+  __shared__ __align__(16) int marks[2][KT + 4];   // tile numbers: of a key with values that are not finite; [KT], of any slight key
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, h2 = lane >> 5;
   const int hk = (int)(blockIdx.x % (uint32_t)g.Hk);
@@ -1095,8 +1113,10 @@ __global__ __launch_bounds__(256, D <= 192 ? 2 : 1) void k_attend_tile(AttendArg
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (pr[2 * KT + 32 * b + 8 * (r >> 2) + 4 * h2 + (r & 3)] == 0.0f)
+          if (const float log = pr[2 * KT + 32 * b + 8 * (r >> 2) + 4 * h2 + (r & 3)]; log < 0.0f) {
             sum[r & 3] += __builtin_amdgcn_exp2f(s[b][r] - kSmallestLog - base);
+            s[b][r] += log;
+          }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {

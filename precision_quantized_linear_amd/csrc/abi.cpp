@@ -1455,7 +1455,7 @@ static pql_status kv_attention_impl(int scheme, const void* q, int64_t ldqt, int
   g.pages = pages;
   g.ldp = ldp;
   g.causal = causal != 0;
-  g.window = (int)(window > (int64_t(1) << 30) ? 0 : window);   // hides nothing: no key is past 2^30
+  g.window = (int)(window > kInt31 ? 0 : window);   // hides nothing: no position is past 2^31 - 2
   g.scale = scale;
   g.out = static_cast<uint16_t*>(out);
   g.ldot = ldot;

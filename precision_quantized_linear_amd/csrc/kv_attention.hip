@@ -83,6 +83,11 @@ __device__ __forceinline__ double wave_sum(double v) {
   return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63), __builtin_amdgcn_readlane(__double2loint(v), 63));
 }
 
+// The first token that a row at `pos` sees; a negative position comes of more new tokens than the cache holds.
+__device__ __forceinline__ int window_begin(const AttendArgs& g, int pos) {
+  return g.window ? std::max(0, std::max(0, pos) - g.window + 1) : 0;
+}
+
 __device__ __forceinline__ int splits_of(int kt, int chunk) { return kt <= chunk ? 1 : (kt + chunk - 1) / chunk; }
 
 // Four consecutive sequences of a lane: their rows, row tiles and the key tiles that any of their rows sees.
@@ -104,7 +109,7 @@ struct Shapes {
     for (int r = 0; r < 4; ++r) {
       qt[r] = (s[r].n * G + BM - 1) / BM;
       const int end = (int)std::min<int64_t>(s[r].len, cap);
-      const int begin = g.window ? std::max(0, s[r].len - s[r].n - g.window + 1) : 0;   // window <= 2^30
+      const int begin = window_begin(g, s[r].len - s[r].n);
       kt[r] = std::max(0, (end + kKeyTile - 1) / kKeyTile - begin / kKeyTile);
     }
   }
@@ -206,8 +211,8 @@ __device__ __forceinline__ Sight sight_of(const AttendArgs& g, const Seq& s, int
   Sight v;
   v.end = g.causal ? std::max(0, std::min(held, hi + 1)) : held;
   v.all_end = g.causal ? std::max(0, std::min(held, lo + 1)) : held;
-  v.begin = g.window ? std::max(0, lo - g.window + 1) : 0;
-  v.all_begin = g.window ? std::max(0, hi - g.window + 1) : 0;
+  v.begin = window_begin(g, lo);
+  v.all_begin = window_begin(g, hi);
   v.kt0 = std::min(v.begin, v.end) / kKeyTile;   // a window past the end (a length past the pages) sees none
   v.kt1 = std::max(v.kt0, (v.end + kKeyTile - 1) / kKeyTile);
   return v;
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
     for (int j = 0; j < D / 32; ++j) qf[n][j] = ldg16(p + 8 * j);
     const int pos = w.s.len - w.s.n + i;
     row_end[n] = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
-    row_begin[n] = g.window ? pos - g.window + 1 : 0;
+    row_begin[n] = window_begin(g, pos);
   }
 
   const float ks0 = score_scale<SCHEME>(g);
@@ -987,11 +992,11 @@ __global__ __launch_bounds__(256, (tile_waves<SCHEME, D>())) void k_attend_tile(
   }
   const int pos = w.s.len - w.s.n + i;
   const int row_end = !live ? 0 : g.causal ? std::min(v.end, pos + 1) : v.end;
-  const int row_begin = g.window ? pos - g.window + 1 : 0;
+  const int row_begin = window_begin(g, pos);
   // the last key that any row of this wave sees, and the first
   const int last = std::min(rows, w.tile * BM + 32 * wave + 32) - 1;
   const int wave_end = g.causal ? std::min(v.end, w.s.len - w.s.n + last / G + 1) : v.end;
-  const int wave_begin = g.window ? w.s.len - w.s.n + (w.tile * BM + 32 * wave) / G - g.window + 1 : 0;
+  const int wave_begin = window_begin(g, w.s.len - w.s.n + (w.tile * BM + 32 * wave) / G);
 
   const float ks0 = score_scale<SCHEME>(g);
   v16f o[ND];

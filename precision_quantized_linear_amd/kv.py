@@ -342,7 +342,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, starts: torch.Tensor, lens: to
     Sequence b has the rows starts[b] .. starts[b + 1] - 1 of q as its last tokens, lens[b] tokens in the
     cache (these included, so ``kv_append`` comes first) and their pages in pages[b] (all int32).  A token
     at position i sees the tokens up to i (``causal``; otherwise all of its sequence) and, with
-    ``window``, only the last ``window`` of those up to i.  H / n_kv_heads consecutive heads share a head
+    ``window``, none before i - ``window`` + 1.  H / n_kv_heads consecutive heads share a head
     of the cache.  ``scale``: on the products, head_dim^-0.5 by default.  Rows of no sequence are left as
     they were in ``out`` (which does not overlap q), or hold anything where it is not given.
     ``workspace``: ``kv_attention_workspace`` bytes, not shared by calls that overlap in time; allocated

@@ -1,5 +1,5 @@
 """Edges of the attention over a paged cache, against the float64 oracle with the bounds of
-tests/kv_check.py: values of extreme sizes.
+tests/kv_check.py: values of extreme sizes, far positions.
 
 Values whose scale lies below 2^-90 are held as weights relative to that, in fp16: a weight (at least 2^7
 for the largest) is off by up to 2^-25 beside its relative error, its code is at most 448, and the sum that
@@ -11,6 +11,7 @@ import torch
 import precision_quantized_linear_amd as pql
 from kv_check import Filled, bf16_bits, check_attention, expected, f64, up16
 from oracle import formats as F
+from oracle import kv as okv
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,25 @@ def test_scales_of_unseen_tokens(scale, new, L):
     got, lse = pql.kv_attention(up16(qb), fill.cache, fill.starts, fill.lens, fill.pages, return_lse=True)
     rows = np.arange(new - 1)
     check_attention(fill, q64, np.where(np.isfinite(f64(got)), f64(got), 1e300), f64(lse), want, rows=rows, small=L)
+
+
+# ---------------------------------------------------------------- far positions
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new", [1, 24, 70])
+@pytest.mark.parametrize("first", [0, 1, 20, 47, 48, 1 << 29])
+def test_windows_of_positions_far_past_the_pages(first, new, causal):
+    """A sequence of 2^31 - 1 tokens, all absent but the first 48: the last token's window, of up to
+    2^31 - 1 tokens, begins at `first`."""
+    rng = np.random.default_rng(6)
+    L, held = (1 << 31) - 1, 48
+    fill = Filled(rng, "fp8_row", [held], 2, 64, 16, [new])
+    fill.lens = torch.tensor([L], dtype=torch.int32, device=fill.lens.device)
+    qb = bf16_bits(rng.standard_normal((new, 4, 64)))
+    q64 = F.bf16_to_f32(qb).astype(np.float64)
+    window = L - first
+    seen = np.arange(held)[None] > np.arange(L - new, L)[:, None] - window
+    want = okv.attend(q64, fill.k[0], fill.v[0], seen, 64 ** -0.5)
+    for w in (window, 1 << 40) if first == 0 else (window,):
+        got, lse = pql.kv_attention(up16(qb), fill.cache, fill.starts, fill.lens, fill.pages, causal=causal, window=w,
+                                    return_lse=True)
+        check_attention(fill, q64, f64(got), f64(lse), want)

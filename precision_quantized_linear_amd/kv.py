@@ -188,12 +188,12 @@ def kv_sizes(scheme: str, n_pages: int, page_size: int, n_kv_heads: int, head_di
 def kv_cache(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, scheme: str = "fp8_row", *,
              k_scale: float | None = None, v_scale: float | None = None, device="cuda") -> KVCache:
     """An empty cache (its memory is not initialised, and needs not be).  "fp8_tensor" takes the two
-    scales it quantizes with, finite and positive."""
+    scales it quantizes with, finite and positive in float32."""
     kv_sizes(scheme, n_pages, page_size, n_kv_heads, head_dim)   # refuses what no cache can be
     given = (k_scale, v_scale)
     if scheme == "fp8_tensor":
-        if any(s is None or not math.isfinite(s) or s <= 0 for s in given):
-            raise ValueError("fp8_tensor needs finite, positive k_scale and v_scale")
+        if any(s is None or not 0.0 < ctypes.c_float(float(s)).value < math.inf for s in given):
+            raise ValueError("fp8_tensor needs k_scale and v_scale, finite and positive in float32")
     elif given != (None, None):
         raise ValueError(f"{scheme} takes no k_scale and v_scale")
     shape = (n_pages, n_kv_heads, page_size, head_dim)

@@ -1350,8 +1350,9 @@ Plan plan_of(const AttendArgs& g) {
   p.parts = 0;
   if (key_tiles <= p.min_chunk) p.target = 0;
   else
-    // a tile of kt > chunk key tiles has at most kt / chunk + 1 < 2 kt / chunk ranges, and chunk >= total Hk / target
-    p.parts = std::min<int64_t>(2 * ((int64_t)p.target / g.Hk + 1) + 32, p.tiles * ((key_tiles + p.min_chunk - 1) / p.min_chunk));
+    // A tile of kt > chunk key tiles has fewer than kt / chunk + 1 < 2 kt / chunk ranges, and chunk >= total Hk / target:
+    // all tiles together fewer than 2 target / Hk.
+    p.parts = std::min<int64_t>(2 * ((int64_t)p.target / g.Hk + 1), p.tiles * ((key_tiles + p.min_chunk - 1) / p.min_chunk));
   return p;
 }
 

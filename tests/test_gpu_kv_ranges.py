@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import precision_quantized_linear_amd as pql
-from kv_check import DEV, Filled, bf16_bits, check_attention, expected, f64, up16
+from kv_check import DEV, SENTINEL, Filled, bf16_bits, check_attention, dev, expected, f64, up16
 from oracle import formats as F
 
 pytestmark = pytest.mark.gpu
@@ -115,3 +115,43 @@ def test_a_broken_token_of_a_cut_context(scheme, new, rows, where):
             elif value != float("inf"):
                 assert np.isnan(seeing).all()
         store[at] = before
+
+
+@pytest.mark.parametrize("scheme", SCHEMES)
+@pytest.mark.parametrize("new,rows", CUT)
+def test_wild_neighbours_of_cut_contexts(scheme, new, rows):
+    """Lengths and pages outside their ranges: the rows of the sequences that have sound ones are exact.  Wild starts
+    besides: no byte outside the operands changes."""
+    rng = np.random.default_rng(5)
+    seqs = [1200, 1300, 1250, 1280]
+    fill = Filled(rng, scheme, seqs, 2, 64, 16, [new] * 4)
+    qb = bf16_bits(rng.standard_normal((fill.T, 4, 64)))
+    q64 = F.bf16_to_f32(qb).astype(np.float64)
+    want = expected(fill, q64)
+
+    def wild(shape):
+        return rng.integers(-(1 << 31), 1 << 31, shape).astype(np.int32)
+
+    def call(starts, lens, pages, **kw):
+        buf = up16(np.full((fill.T + 8, 4, 64), SENTINEL, np.uint16))
+        _, lse = attend_cut(fill, up16(qb), rows, starts=starts, lens=lens, pages=pages, out=buf[4: 4 + fill.T],
+                            return_lse=True, **kw)
+        edge = buf.view(torch.int16)
+        assert (edge[:4] == SENTINEL).all() and (edge[-4:] == SENTINEL).all()
+        return f64(buf[4: 4 + fill.T]), f64(lse)
+
+    for step in range(6):
+        lens, pages = np.array(seqs, np.int32), fill.pages_np.copy()
+        bad = rng.permutation(4)[:2]
+        if step % 3 != 1:
+            lens[bad] = wild(2) if step < 3 else [(1 << 31) - 1, -1]
+        if step % 3 != 0:
+            pages[bad] = wild(pages[bad].shape)
+        sound = np.concatenate([np.arange(b * new, (b + 1) * new) for b in range(4) if b not in bad])
+        got, lse = call(fill.starts, dev(lens), dev(pages))
+        check_attention(fill, q64, np.where(np.isfinite(got), got, 1e30), lse, want, rows=sound)
+        call(dev(wild(5)), dev(lens), dev(pages), cut=False)
+        call(dev(np.sort(wild(5))), dev(lens), dev(pages), cut=False)
+    T = fill.T
+    for starts in ([0, T, 0, T, 0], [T, 0, T, 0, T], [0, T, T, T, T], [-5, T, -7, T + 9, 3]):
+        call(dev(np.array(starts, np.int32)), fill.lens, fill.pages, cut=False)

@@ -442,8 +442,14 @@ const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, in
  * starts are cut to 0 .. T, negative lens to 0, and tokens past the width pages
  * or on a page outside 0 .. n_pages - 1 are absent.
  * Row strides ld*t (token) and ld*h (head) are in elements, any multiples of 8;
- * the D values of a head are contiguous and start on 16 bytes.  T * H <= 2^31 - 1,
- * B <= 2^20, width * page_size <= 2^30. */
+ * the D values of a head are contiguous and start on 16 bytes.
+ * Limits: T * H * D <= 2^34 (T * Hk * D where keys and values are appended,
+ * n * Hk * D where they are read; T <= 2^31 - 1 for pql_kv_slots), B <= 2^20,
+ * width * page_size <= 2^30, (B - 1) * ldp <= 2^40, 2^40 values in a half of a cache
+ * or from the first to the last of an operand.  pql_kv_attention: H <= 65535, and fewer than 2^24
+ * workgroups, T * H / r + min(B, T) * Hk of which are its tiles of r = 16, 32 or
+ * 128 rows (a single token for each of 2^20 sequences with 15 heads of the cache
+ * is within, with 16 not); pql_kv_attention_workspace refuses what is past it. */
 
 typedef enum pql_kv_scheme { PQL_KV_BF16 = 0, PQL_KV_FP8_TENSOR = 1, PQL_KV_FP8_ROW = 2 } pql_kv_scheme;
 

@@ -1,4 +1,5 @@
-"""The borders of what the calls around the cache of keys and values accept: given scales in fp32.  No GPU needed."""
+"""The borders of what the calls around the cache of keys and values accept: given scales in fp32, workspaces,
+sizes.  No GPU needed."""
 import math
 
 import pytest
@@ -31,3 +32,58 @@ def test_a_workspace_holds_no_more_ranges_than_there_can_be(H, Hk, T, B, rows):
     assert ("tile" if rows == 128 else f"<{rows}>") in name and "join" in name
     places = pql.kv_attention_workspace("fp8_row", T, H, Hk, 128, B, width, 16) / (Hk * rows * (128 + 4) * 4)
     assert 0 < places <= 2 * ((767 if rows == 128 else 9 * 256) // Hk + 1)
+
+
+# ---------------------------------------------------------------- sizes: the last one taken and the first refused
+# Calls that pass the checks of sizes are refused for their NULL operands: nothing is ever launched.
+NULL = "must be non-NULL"
+
+
+def refusal(status):
+    assert status == pql.PQL_ERR_INVALID_ARGUMENT
+    return pql.lib().pql_last_error().decode()
+
+
+@pytest.mark.parametrize("D,T,H,fits", [(64, 1 << 28, 1, True), (64, (1 << 28) + 1, 1, False), (64, 1 << 20, 1 << 8, True),
+                                        (64, 1 << 20, (1 << 8) + 1, False), (256, 1 << 26, 1, True), (256, 1 << 25, 3, False),
+                                        (16, 1 << 30, 1, True), (16, (1 << 30) + 1, 1, False), (1024, 1 << 24, 1, True),
+                                        (1024, 1 << 23, 3, False)])
+def test_rope_sizes(D, T, H, fits):
+    text = refusal(pql.lib().pql_rope(0, None, T, H, D, H * D, D, 1 << 20, 1 << 20, 16, 1.0, None, H * D, D, None))
+    assert (NULL in text) == fits and ("too large" in text) != fits
+
+
+@pytest.mark.parametrize("D,n,Hk,fits", [(64, 1 << 27, 2, True), (64, (1 << 27) + 1, 2, False), (256, 1 << 20, 64, True),
+                                         (256, (1 << 20) + 1, 64, False)])
+def test_append_and_read_sizes(D, n, Hk, fits):
+    st = (Hk * D, D)
+    for status in (pql.lib().pql_kv_append(2, None, *st, None, *st, n, None, 0, None, None, 0, 1.0, None, None, None, None,
+                                           4, 16, Hk, D, None),
+                   pql.lib().pql_kv_read(2, None, None, None, None, 4, 16, Hk, D, None, n, None, *st, None, *st, None)):
+        text = refusal(status)
+        assert (NULL in text) == fits and ("too large" in text) != fits
+
+
+@pytest.mark.parametrize("T,H,Hk,D,B,fits", [
+    (1, 65535, 1, 64, 1, True), (1, 65536, 1, 64, 1, False), (1 << 20, 256, 8, 64, 1, True), ((1 << 20) + 1, 256, 8, 64, 1, False),
+    (1 << 20, 15, 15, 64, 1 << 20, True), (1 << 20, 16, 16, 64, 1 << 20, False), (1, 1, 1, 256, 1 << 20, True),
+    (1, 1, 1, 256, (1 << 20) + 1, False),
+])
+def test_attention_sizes(T, H, Hk, D, B, fits):
+    assert bool(pql.kv_kernel_name("fp8_row", T, H, Hk, D, B, 1, 16)) == fits
+    if fits:
+        pql.kv_attention_workspace("fp8_row", T, H, Hk, D, B, 1, 16)
+    else:
+        with pytest.raises(ValueError):
+            pql.kv_attention_workspace("fp8_row", T, H, Hk, D, B, 1, 16)
+
+
+def test_batch_sizes():
+    L = pql.lib()
+    assert NULL in refusal(L.pql_kv_slots(None, None, None, 1 << 20, 1, 1 << 20, 16, 4, None, None, None))
+    assert "ldp must" in refusal(L.pql_kv_slots(None, None, None, 1 << 20, 1, (1 << 20) + 2, 16, 4, None, None, None))
+    assert NULL in refusal(L.pql_kv_slots(None, None, None, 1, 1 << 26, 1 << 26, 16, 4, None, None, None))
+    assert "width" in refusal(L.pql_kv_slots(None, None, None, 1, (1 << 26) + 1, 1 << 27, 16, 4, None, None, None))
+    assert "B must" in refusal(L.pql_kv_slots(None, None, None, (1 << 20) + 1, 1, 1, 16, 4, None, None, None))
+    assert NULL in refusal(L.pql_kv_slots(None, None, None, 1, 1, 1, 16, (1 << 31) - 1, None, None, None))
+    assert "T must" in refusal(L.pql_kv_slots(None, None, None, 1, 1, 1, 16, 1 << 31, None, None, None))

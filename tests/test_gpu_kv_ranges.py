@@ -155,3 +155,36 @@ def test_wild_neighbours_of_cut_contexts(scheme, new, rows):
     T = fill.T
     for starts in ([0, T, 0, T, 0], [T, 0, T, 0, T], [0, T, T, T, T], [-5, T, -7, T + 9, 3]):
         call(dev(np.array(starts, np.int32)), fill.lens, fill.pages, cut=False)
+
+
+@pytest.mark.parametrize("scheme", SCHEMES)
+@pytest.mark.parametrize("new,rows", CUT)
+def test_cut_contexts_in_a_captured_call(scheme, new, rows):
+    """Captured once, replayed over contexts of other lengths (some not cut at all) with eager calls between:
+    the same bits as the eager call's, which the tests above hold to the oracle."""
+    rng = np.random.default_rng(6)
+    fill = Filled(rng, scheme, [2600, 700], 2, 64, 16, [new, new])
+    q = torch.zeros((fill.T, 4, 64), dtype=torch.bfloat16, device=DEV)
+    lens = fill.lens.clone()
+
+    def call():
+        return attend_cut(fill, q, rows, lens=lens, cut=False, return_lse=True)
+
+    def eager_bits():
+        return [t.view(torch.uint8).cpu() for t in call()]
+
+    q.copy_(up16(bf16_bits(rng.standard_normal(q.shape))))
+    eager_bits()
+    size = (scheme, fill.T, 4, 2, 64, 2, fill.pages.shape[1], 16)
+    ws = torch.empty((pql.kv_attention_workspace(*size),), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pql.kv_attention(q, fill.cache, fill.starts, lens, fill.pages, return_lse=True, workspace=ws)
+    for step in ([2600, 700], [100, 90], [2599, 0], [1900, 650], [90, 700], [2600, 700]):
+        lens.copy_(dev(np.array(step, np.int32)))
+        q.copy_(up16(bf16_bits(rng.standard_normal(q.shape))))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.view(torch.uint8).cpu() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, eager_bits()))

@@ -758,10 +758,11 @@ __global__ __launch_bounds__(256, (stream_waves<SCHEME, D, NQ>())) void k_attend
 // way to LDS (values transposed, so that a fragment of either operand is one 16-byte read), and
 // double-buffered: one barrier per tile.
 //
-// Bound by what lies between the products: 8192 new tokens over 32768, 32 heads of 128, run at 820 to 850 TFLOP/s
-// (4.53 to 4.70 ms), three quarters of a large bf16 library product.
-// Vector instructions issue 49 % of the time and matrix products 37 %; without staging it would be 22 % faster,
-// without the exponentials 5 %, without the second product no faster.  32 rows per wave, because O, q and a tile's
+// Bound by what lies between the products: 8192 new tokens over 32768, 32 heads of 128, run at 800 to 850 TFLOP/s
+// (4.53 to 4.82 ms from card to card), three quarters of a large bf16 library product.
+// Vector instructions issue 53 % of the time, LDS is busy 50 % (bank conflicts 9 %), the matrix cores 36 %; copies that
+// leave a step out are faster by 22 % (staging; its stores to LDS alone 11), 18 (the second product) and 6 (the
+// exponentials).  32 rows per wave, because O, q and a tile's
 // scores for 64 do not fit in registers beside the loads (spills: slower), and four waves, because eight on a tile of
 // 256 rows leave one workgroup per CU (five chunks of 300: 103 -> 121 us).
 template <int SCHEME, int D>
@@ -1302,7 +1303,8 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs g) {
 // kernel has half the waves or half the key tile (256 values, 8 sequences, 64 rows: 78 | 81 | 141, 128:
 // 124 | 113 | 149, 256: 203 | 174 | 199), so that few rows reach further there; up to 128 rows, because many
 // short contexts, which the host can not tell, want tiles of 128 earlier (32 of 600 tokens, bf16, 128 rows: 86 |
-// 81 | 62).
+// 81 | 62).  The mean serves a batch of like sequences: a chunk of 2048 beside 60 single tokens over 8192 takes tiles of 128
+// for all, 642 us where two calls take 210 + 337, one of 256 beside them tiles of 16 for all, 305 for 210 + 63.
 struct Plan {
   int bm;
   int target, min_chunk;
@@ -1328,7 +1330,10 @@ Plan plan_of(const AttendArgs& g) {
   p.tiles = rows / p.bm + seqs;
   // Ranges in rounds of the workgroups that fit on the card: each row tile's last range is half a range short
   // on average, so that `target` full ones make target + tiles / 2.  Many rows: as few rounds as leave half of
-  // the last one's ranges full (five chunks of 300: 96 -> 76 us).  Few rows: one round where few row tiles share
+  // the last one's ranges full (five chunks of 300: 96 -> 76 us), of 512 at every head size, though one workgroup per CU
+  // fits at 256 values and three of FP8 at 64.  Rounds of 256 and 768 there: 256 values, 512 over 16384: 344 -> 327, 8 x 64
+  // over 8192: 210 -> 196, uncut contexts level; 64 values, 5 x 300 over 12000: 170 -> 140, but 3 x 700 over 9000: 190 ->
+  // 198, 32 x 128 over 2000: 84 -> 88.  Few rows: one round where few row tiles share
   // the card (one token over 131000, in ranges: 512: 64, 768: 63, 1024: 75), three where ranges of many
   // sequences have to even out (64 sequences up to 16384, 768: 157, 1536: 134, 2304: 129).
   //

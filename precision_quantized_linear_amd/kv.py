@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import sys
 from dataclasses import dataclass
 
 import torch
@@ -72,6 +73,8 @@ def rope_freqs(dim: int, base: float = 10000.0, *, layout: str = "half", scaling
     if not (s >= 1.0 and math.isfinite(s)):
         raise ValueError(f"factor must be a finite number from 1 on (got {s!r})")
     if kind == "ntk":
+        if math.log(base) + math.log(s) * dim / (dim - 2) >= math.log(sys.float_info.max):
+            raise ValueError(f"ntk scaling needs a factor whose base is finite (got {s!r})")
         base *= s ** (dim / (dim - 2))
     pairs = torch.arange(dim // 2, dtype=torch.float64)
     f = base ** (-2.0 * pairs / dim)
@@ -84,12 +87,17 @@ def rope_freqs(dim: int, base: float = 10000.0, *, layout: str = "half", scaling
         if not (span > 0 and fast > slow > 0):
             raise ValueError(f"{kind} scaling needs original > 0 and fast > slow > 0")
         if kind == "yarn":
+            if not (math.isfinite(span) and math.isfinite(fast)):
+                raise ValueError("yarn scaling needs finite original and fast")
+
             def pair_of(turns):   # the (real) index whose frequency turns so often over `original` positions
                 return dim * math.log(span / (2 * math.pi * turns)) / (2 * math.log(base))
             lo = max(math.floor(pair_of(fast)), 0)
             hi = min(math.ceil(pair_of(slow)), dim - 1)
             keep = 1.0 - ((pairs - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
             scale = float(scaling.get("attention", 0.1 * math.log(s) + 1.0))
+            if not math.isfinite(ctypes.c_float(scale).value):
+                raise ValueError(f"yarn scaling needs an attention that is finite in float32 (got {scale!r})")
         else:
             keep = ((span * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
         f = f * keep + f / s * (1.0 - keep)

@@ -87,3 +87,15 @@ def test_batch_sizes():
     assert "B must" in refusal(L.pql_kv_slots(None, None, None, (1 << 20) + 1, 1, 1, 16, 4, None, None, None))
     assert NULL in refusal(L.pql_kv_slots(None, None, None, 1, 1, 1, 16, (1 << 31) - 1, None, None, None))
     assert "T must" in refusal(L.pql_kv_slots(None, None, None, 1, 1, 1, 16, 1 << 31, None, None, None))
+
+
+# ---------------------------------------------------------------- rotary tables
+@pytest.mark.parametrize("scaling", [
+    dict(type="yarn", factor=2.0, original=math.inf), dict(type="yarn", factor=2.0, original=4096, fast=math.inf),
+    dict(type="yarn", factor=2.0, original=4096, attention=math.nan), dict(type="yarn", factor=2.0, original=4096, attention=math.inf),
+    dict(type="yarn", factor=2.0, original=4096, attention=1e39), dict(type="ntk", factor=1e300),
+])
+def test_stretching_that_leaves_the_numbers_range(scaling):
+    """Refused by name where the table is made, not as an overflow there or by a later call."""
+    with pytest.raises(ValueError, match=scaling["type"] + " scaling needs"):
+        pql.rope_freqs(64, scaling=scaling)

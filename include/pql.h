@@ -445,11 +445,12 @@ const char* pql_moe_kernel_name(int scheme, int gather, int64_t T, int64_t k, in
  * the D values of a head are contiguous and start on 16 bytes.
  * Limits: T * H * D <= 2^34 (T * Hk * D where keys and values are appended,
  * n * Hk * D where they are read; T <= 2^31 - 1 for pql_kv_slots), B <= 2^20,
- * width * page_size <= 2^30, (B - 1) * ldp <= 2^40, 2^40 values in a half of a cache
- * or from the first to the last of an operand.  pql_kv_attention: H <= 65535, and fewer than 2^24
- * workgroups, T * H / r + min(B, T) * Hk of which are its tiles of r = 16, 32 or
- * 128 rows (a single token for each of 2^20 sequences with 15 heads of the cache
- * is within, with 16 not); pql_kv_attention_workspace refuses what is past it. */
+ * width * page_size <= 2^30, (B - 1) * ldp <= 2^40, 2^40 values in a half of a
+ * cache or from the first to the last of an operand.  pql_kv_attention:
+ * H <= 65535, and fewer than 2^24 workgroups, T * H / r + min(B, T) * Hk of which
+ * are its tiles of r = 16, 32 or 128 rows (a single token for each of 2^20
+ * sequences with 15 heads of the cache is within, with 16 not);
+ * pql_kv_attention_workspace refuses what is past it. */
 
 typedef enum pql_kv_scheme { PQL_KV_BF16 = 0, PQL_KV_FP8_TENSOR = 1, PQL_KV_FP8_ROW = 2 } pql_kv_scheme;
 
@@ -515,8 +516,10 @@ pql_status pql_kv_attention_workspace(int scheme, int64_t T, int64_t H, int64_t 
  * j runs over the sequence's tokens; with causal != 0 a token at position i
  * sees j <= i, with window > 0 only j > i - window.  q: bf16 [T, H, D]; scores,
  * sums and the joining of a split context are fp32, the weights p enter the
- * matrix cores in 16 bits (fp16 for FP8 caches, bf16 for KV_BF16), one rounding to bf16 at
- * the end.  lse (fp32 [T, H], contiguous, or NULL) receives log sum_j exp(scale q . k_j).
+ * matrix cores in 16 bits (fp16 for FP8 caches, where one that is, with its value's
+ * scale, below 2^-21 of its row's largest is exact to 2^-32 of that; bf16 for
+ * KV_BF16), one rounding to bf16 at the end.  lse (fp32 [T, H], contiguous, or
+ * NULL) receives log sum_j exp(scale q . k_j).
  * A token that sees nothing gets zeros and an lse of -inf.  Rows of no sequence
  * are left as they were.  out and q do not overlap.  A NaN or an infinity in
  * the cache reaches only the tokens that see it, possibly all of their D values.

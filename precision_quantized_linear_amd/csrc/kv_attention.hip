@@ -956,7 +956,7 @@ struct KeyTile {
 };
 
 // Workgroups per CU.  192 values with a scale per token spill 12 registers at two, and one is slower still (4096 new
-// tokens over 8192, 16 heads: 763 | 871 us; 512 over 16384: 223 | 313); 64 values of FP8 need one register less for three.
+// tokens over 8192, 16 heads: 763 | 871 us; 512 over 16384: 223 | 313).  64 values of FP8 left alone take one register too many for three.
 template <int SCHEME, int D>
 constexpr int tile_waves() { return D == 64 && SCHEME != kKvBf16 ? 3 : D <= 192 ? 2 : 1; }
 
